@@ -150,7 +150,7 @@ def _quantise(x):
     g = x.to(F32).reshape(*x.shape[:-1], D // GROUP, GROUP)
     low, high = g.amin(-1, keepdim=True).clamp(max=0), g.amax(-1, keepdim=True).clamp(min=0)
     step = (high - low) * 16 / torch.full_like(low, 15.0)   # by a tensor: rounded once, as the definition has it
-    step = ((step.view(torch.int32) + 0xFFFFF) & ~0xFFFFF).view(F32).clamp(2.0 ** -14, 61440.0)   # up to 4 bits
+    step = ((step.view(torch.int32) + 0xFFFFF) & ~0xFFFFF).view(F32).clamp(2.0 ** -14, 12288.0)   # up to 4 bits
     s = step / 16
     z = torch.round(-low / s).clamp(0, 15)
     u = (torch.round(g / s) + z).clamp(0, 15).to(torch.uint8)
@@ -450,7 +450,7 @@ def _exact_write(case, s):
         low, high = g.min(-1, keepdim=True)[0].clamp(max=0), g.max(-1, keepdim=True)[0].clamp(min=0)
         need = (high - low).clamp(min=2.0 ** -60) / 15
         e = torch.floor(torch.log2(need)) - 3                            # the step: up to 4 significant bits
-        step = (torch.ceil(need / torch.exp2(e)) * torch.exp2(e)).clamp(2.0 ** -18, 3840.0)
+        step = (torch.ceil(need / torch.exp2(e)) * torch.exp2(e)).clamp(2.0 ** -18, 768.0)
         z = (-low / step).round().clamp(0, 15)
         y = (((g / step).round() + z).clamp(0, 15) - z) * step
         y = y.reshape(B, W, heads, D)
