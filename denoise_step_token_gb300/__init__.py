@@ -14,6 +14,11 @@ Names follow the C ABI in ``include/dllm.h``:
 * ``pack``      -- the left-padded box (BlockServe page, section II-E).
 * ``advance``   -- block commit and eviction flags (BlockServe Algorithm 1).
 * ``compact``   -- stable in-place compaction (FDFO eviction).
+* ``token_logprobs`` -- log probabilities of given tokens over the step's
+  logits, entropy and the best alternatives.
+* ``kv4_pages`` / ``kv4_write`` / ``kv4_attend`` / ``kv4_evict`` -- the paged
+  cache of keys and values in 4 bits: its pool, the write, a block's
+  attention over it, and its thinning by attention weight.
 """
 from __future__ import annotations
 
@@ -27,6 +32,7 @@ import numpy as np
 from . import _build
 
 __all__ = ["load", "step", "step_host", "features", "pack_plan", "admit", "pack", "advance", "compact", "refill",
+           "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict",
            "get_device_error", "DllmError", "NUM_FEATURES", "LIB_PATH"]
 
 LIB_PATH = _build.LIB_PATH
@@ -108,6 +114,36 @@ class RefillArgs(ctypes.Structure):
                 ("rid", _p), ("p", _p), ("b", _p), ("K", _p), ("thr", _p), ("input_ids", _p), ("conf_state", _p)]
 
 
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [("N", _i32), ("V", _i32), ("top", _i32), ("dtype", _i32), ("ldv", _i64), ("logits_rows", _i64),
+                ("logits", _p), ("rows", _p), ("tokens", _p), ("logprob", _p), ("entropy", _p), ("top_ids", _p),
+                ("top_logprobs", _p), ("workspace", _p), ("workspace_bytes", _sz)]
+
+
+class Kv4Cache(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("heads", _i32), ("page_size", _i32), ("head_dim", _i32), ("B", _i32),
+                ("max_pages", _i32), ("pages", _p), ("table", _p)]
+
+
+class Kv4WriteArgs(ctypes.Structure):
+    _fields_ = [("cache", Kv4Cache), ("W", _i32), ("pad0", _i32), ("k", _p), ("v", _p), ("k_stride", _i64 * 3),
+                ("v_stride", _i64 * 3), ("pos", _p), ("first", _p), ("count", _p), ("k_out", _p), ("v_out", _p)]
+
+
+class Kv4AttendArgs(ctypes.Structure):
+    _fields_ = [("cache", Kv4Cache), ("L", _i32), ("q_heads", _i32), ("scale", ctypes.c_float), ("pad0", _i32),
+                ("q", _p), ("q_stride", _i64 * 3), ("lens", _p), ("out", _p), ("lse", _p), ("prior", _p),
+                ("weights", _p), ("workspace", _p), ("workspace_bytes", _sz)]
+
+
+class Kv4EvictArgs(ctypes.Structure):
+    _fields_ = [("cache", Kv4Cache), ("recent", _i32), ("dst_max_pages", _i32), ("lens", _p), ("keep", _p),
+                ("weights", _p), ("dst_table", _p), ("dst_lens", _p), ("src", _p)]
+
+
+MAX_TOP = 32
+KV4_GROUP = 32
+
 _lib = None
 _lock = threading.Lock()
 
@@ -162,6 +198,13 @@ _SIGNATURES = {
     "dllm_compact_workspace_size": (_sz, [_i32, _i32, _p]),
     "dllm_compact": (ctypes.c_int, [ctypes.POINTER(CompactArgs), _p]),
     "dllm_refill": (ctypes.c_int, [ctypes.POINTER(RefillArgs), _p]),
+    "dllm_logprobs_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "dllm_logprobs": (ctypes.c_int, [ctypes.POINTER(LogprobsArgs), _p]),
+    "dllm_kv4_page_bytes": (_sz, [_i32, _i32]),
+    "dllm_kv4_write": (ctypes.c_int, [ctypes.POINTER(Kv4WriteArgs), _p]),
+    "dllm_kv4_attend_workspace_size": (_sz, [ctypes.POINTER(Kv4Cache), _i32, _i32]),
+    "dllm_kv4_attend": (ctypes.c_int, [ctypes.POINTER(Kv4AttendArgs), _p]),
+    "dllm_kv4_evict": (ctypes.c_int, [ctypes.POINTER(Kv4EvictArgs), _p]),
 }
 
 
@@ -198,7 +241,8 @@ def load(build=True):
         if lib.dllm_abi_version() != ABI_VERSION:
             raise RuntimeError(f"libdllm ABI version {lib.dllm_abi_version()}, binding expects {ABI_VERSION}")
         for which, cls in enumerate((StepArgs, PackArgs, CompactArgs, AdvanceArgs, RefillArgs, LoopConfig, LoopInfo,
-                                     VocabShard, LoopControl)):
+                                     VocabShard, LoopControl, LogprobsArgs, Kv4Cache, Kv4WriteArgs, Kv4AttendArgs,
+                                     Kv4EvictArgs)):
             if lib.dllm_struct_size(which) != ctypes.sizeof(cls):
                 raise RuntimeError(f"ABI mismatch for {cls.__name__}: library {lib.dllm_struct_size(which)} "
                                    f"bytes, binding {ctypes.sizeof(cls)}")
@@ -646,3 +690,198 @@ def refill(A0, new_rid, new_p, new_K, new_thr, rid, p, b, K, thr, input_ids, con
                    new_K=_ptr(new_K), new_thr=_ptr(new_thr), rid=_ptr(rid), p=_ptr(p), b=_ptr(b), K=_ptr(K),
                    thr=_ptr(thr), input_ids=_ptr(input_ids), conf_state=_ptr(conf_state))
     _check("dllm_refill", load().dllm_refill(ctypes.byref(a), _stream(dev)))
+
+
+# ---------------------------------------------------------------------------
+# operators around the step: token reports and the 4-bit cache
+# ---------------------------------------------------------------------------
+_stream_ws = {}
+
+
+def _workspace(device, nbytes):
+    """A zero-initialised workspace of this device's current stream, grown on
+    demand (calls on different streams may overlap: each has its own)."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(device).cuda_stream
+    cur = _stream_ws.get((device.index, stream))
+    if cur is None or cur.numel() < nbytes:
+        cur = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        _stream_ws[(device.index, stream)] = cur
+    return cur
+
+
+def token_logprobs(logits, tokens, *, V=None, top=0, rows=None, workspace=None):
+    """Log probabilities of given tokens, entropy and the best alternatives
+    (dllm_logprobs) on the current stream.
+
+    logits:    bf16 or float32 CUDA tensor of rows (last dimension the row
+               stride, 16-byte rows), V (default: the stride) values each
+    tokens:    int32 [N], the token asked for in each entry (-1: none)
+    rows:      int32 [N] row of each entry, or None: entry i is row i
+    top:       alternatives per entry, 0 to MAX_TOP
+    workspace: uint8 CUDA tensor of dllm_logprobs_workspace_size bytes, zeroed
+               once; default: one kept for the current stream
+    Returns a dict: logprob and entropy (float32 [N]) and, with top, top_ids
+    (int32 [N, top]) and top_logprobs (float32 [N, top]), largest first."""
+    torch = _torch()
+    dev = _require_cuda(logits, tokens, rows)
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits must be bf16 or float32")
+    if tokens.dtype != torch.int32 or (rows is not None and rows.dtype != torch.int32):
+        raise TypeError("tokens and rows int32 expected")
+    N = tokens.numel()
+    ldv = logits.shape[-1]
+    n_rows = logits.numel() // ldv if ldv else 0
+    if (rows.numel() if rows is not None else N) != N or (rows is None and n_rows < N):
+        raise ValueError("one row per token")
+    out = {"logprob": torch.empty(N, dtype=torch.float32, device=dev),
+           "entropy": torch.empty(N, dtype=torch.float32, device=dev)}
+    if top > 0:
+        out["top_ids"] = torch.empty((N, top), dtype=torch.int32, device=dev)
+        out["top_logprobs"] = torch.empty((N, top), dtype=torch.float32, device=dev)
+    lib = load()
+    V = ldv if V is None else V
+    ws = workspace
+    if ws is None:
+        ws = _workspace(dev, lib.dllm_logprobs_workspace_size(N, V, top))
+    a = LogprobsArgs(N, V, top, 0 if logits.dtype == torch.bfloat16 else 1, ldv, n_rows, logits.data_ptr(),
+                     None if rows is None else rows.data_ptr(), tokens.data_ptr(), out["logprob"].data_ptr(),
+                     out["entropy"].data_ptr(), out["top_ids"].data_ptr() if top > 0 else None,
+                     out["top_logprobs"].data_ptr() if top > 0 else None, ws.data_ptr(), ws.numel())
+    _check("dllm_logprobs", lib.dllm_logprobs(ctypes.byref(a), _stream(dev)))
+    return out
+
+
+def kv4_pages(n_pages, heads, page_size, head_dim, device):
+    """A pool for the 4-bit cache: (pages uint8 [n_pages, heads, bytes],
+    weights float32 [n_pages, heads, page_size]), both zero."""
+    torch = _torch()
+    nbytes = int(load().dllm_kv4_page_bytes(page_size, head_dim))
+    if nbytes == 0 or n_pages < 1 or heads < 1:
+        raise ValueError("page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; at least one page and head")
+    return (torch.zeros((n_pages, heads, nbytes), dtype=torch.uint8, device=device),
+            torch.zeros((n_pages, heads, page_size), dtype=torch.float32, device=device))
+
+
+def _kv4_cache(pages, table, page_size, head_dim):
+    torch = _torch()
+    if pages.dtype != torch.uint8 or pages.dim() != 3:
+        raise TypeError("pages must be uint8 [n_pages, heads, bytes]")
+    if table.dtype != torch.int32 or table.dim() != 2:
+        raise TypeError("the page table must be int32 [B, max_pages]")
+    n_pages, heads, nbytes = pages.shape
+    if nbytes != page_size * (head_dim + head_dim // 8):
+        raise ValueError("pages do not hold whole pages of this head_dim")
+    return Kv4Cache(n_pages, heads, page_size, head_dim, table.shape[0], table.shape[1], pages.data_ptr(),
+                    table.data_ptr())
+
+
+def _int32_rows(name, t, n):
+    torch = _torch()
+    if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+        raise TypeError(f"{name} must be int32 [{n}]")
+
+
+def kv4_write(k, v, pages, table, pos, *, first=None, count=None, k_out=None, v_out=None):
+    """Write keys and values into the 4-bit cache (dllm_kv4_write) on the
+    current stream.
+
+    k, v:     bf16 [B, W, heads, D], channels contiguous (a slice of a fused
+              projection will do)
+    pages:    the pool (kv4_pages); table: int32 [B, max_pages]
+    pos:      int32 [B] cache position of the first written column
+    first:    int32 [B] first written column (default 0)
+    count:    int32 [B] columns written (default: all from ``first``)
+    k_out, v_out: bf16 [B, W, heads, D] or None: what the cache now holds, in
+              the written columns"""
+    torch = _torch()
+    dev = _require_cuda(pages, table, pos, first, count, k_out, v_out)
+    if k.device != dev or v.device != dev:
+        raise ValueError("tensors live on different devices")
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 4 or k.shape != v.shape:
+        raise TypeError("k and v must be bf16 [B, W, heads, D]")
+    B, W, heads, D = k.shape
+    if k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("the channels of k and v must be contiguous")
+    if table.shape[0] != B or pages.shape[1] != heads:
+        raise ValueError("k, v, pages and table disagree about requests or heads")
+    for name, t in (("pos", pos), ("first", first), ("count", count)):
+        _int32_rows(name, t, B)
+    for t in (k_out, v_out):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != k.shape):
+            raise TypeError("k_out and v_out must be bf16 like k")
+    a = Kv4WriteArgs(_kv4_cache(pages, table, pages.shape[2] // (D + D // 8), D), W, 0, k.data_ptr(), v.data_ptr(),
+                     (_i64 * 3)(*k.stride()[:3]), (_i64 * 3)(*v.stride()[:3]), pos.data_ptr(),
+                     None if first is None else first.data_ptr(), None if count is None else count.data_ptr(),
+                     None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr())
+    _check("dllm_kv4_write", load().dllm_kv4_write(ctypes.byref(a), _stream(dev)))
+
+
+def kv4_attend(q, pages, table, lens, *, scale=None, prior=None, weights=None, workspace=None):
+    """Attention of a block's queries over the 4-bit cache (dllm_kv4_attend) on
+    the current stream.
+
+    q:       bf16 [B, L, q_heads, D], channels contiguous
+    lens:    int32 [B] cached tokens of each request
+    scale:   of the scores, default 1 / sqrt(D)
+    weights: float32 [n_pages, heads, page_size] or None: receives what every
+             cached token was given by its head's queries, plus ``prior`` (the
+             same tensor will do; None: 0)
+    Returns a dict: out (bf16 like q, contiguous), lse (float32 [B, L,
+    q_heads]) and, where given, weights."""
+    torch = _torch()
+    dev = _require_cuda(pages, table, lens, prior, weights)
+    if q.device != dev:
+        raise ValueError("tensors live on different devices")
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.stride(3) != 1:
+        raise TypeError("q must be bf16 [B, L, q_heads, D] with contiguous channels")
+    B, L, q_heads, D = q.shape
+    page_size = pages.shape[2] // (D + D // 8)
+    if table.shape[0] != B:
+        raise ValueError("q and table disagree about the requests")
+    _int32_rows("lens", lens, B)
+    for t in (prior, weights):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (pages.shape[0], pages.shape[1], page_size)):
+            raise TypeError("prior and weights must be float32 [n_pages, heads, page_size]")
+    cache = _kv4_cache(pages, table, page_size, D)
+    out = {"out": torch.empty((B, L, q_heads, D), dtype=torch.bfloat16, device=dev),
+           "lse": torch.empty((B, L, q_heads), dtype=torch.float32, device=dev)}
+    if weights is not None:
+        out["weights"] = weights
+    lib = load()
+    ws = workspace
+    if ws is None:
+        ws = _workspace(dev, lib.dllm_kv4_attend_workspace_size(ctypes.byref(cache), L, q_heads))
+    a = Kv4AttendArgs(cache, L, q_heads, D ** -0.5 if scale is None else scale, 0, q.data_ptr(),
+                      (_i64 * 3)(*q.stride()[:3]), lens.data_ptr(), out["out"].data_ptr(), out["lse"].data_ptr(),
+                      None if prior is None else prior.data_ptr(), None if weights is None else weights.data_ptr(),
+                      ws.data_ptr(), ws.numel())
+    _check("dllm_kv4_attend", lib.dllm_kv4_attend(ctypes.byref(a), _stream(dev)))
+    return out
+
+
+def kv4_evict(pages, weights, table, lens, keep, dst_table, *, recent=0):
+    """Evict the least attended tokens of the 4-bit cache (dllm_kv4_evict) on
+    the current stream: of each request and head the last ``recent`` tokens and
+    the largest weights among the others, ``keep[b]`` in all, move in their
+    order to the pages of ``dst_table`` (not among the source pages), with
+    their weights.  The source pages are the caller's to free afterwards.
+    Returns a dict: lens (int32 [B], the new lengths) and src (int32 [B, heads,
+    dst_max_pages * page_size], where each token came from; -1 past the end)."""
+    torch = _torch()
+    dev = _require_cuda(pages, weights, table, lens, keep, dst_table)
+    if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[:2] != pages.shape[:2]:
+        raise TypeError("weights must be float32 [n_pages, heads, page_size]")
+    B, page_size = table.shape[0], weights.shape[2]
+    D = pages.shape[2] // page_size * 8 // 9
+    if dst_table.dtype != torch.int32 or dst_table.dim() != 2 or dst_table.shape[0] != B:
+        raise TypeError("dst_table must be int32 [B, dst_max_pages]")
+    _int32_rows("lens", lens, B)
+    _int32_rows("keep", keep, B)
+    heads, most = pages.shape[1], dst_table.shape[1]
+    out = {"lens": torch.empty(B, dtype=torch.int32, device=dev),
+           "src": torch.empty((B, heads, most * page_size), dtype=torch.int32, device=dev)}
+    a = Kv4EvictArgs(_kv4_cache(pages, table, page_size, D), recent, most, lens.data_ptr(), keep.data_ptr(),
+                     weights.data_ptr(), dst_table.data_ptr(), out["lens"].data_ptr(), out["src"].data_ptr())
+    _check("dllm_kv4_evict", load().dllm_kv4_evict(ctypes.byref(a), _stream(dev)))
+    return out

@@ -104,6 +104,11 @@ extern "C" size_t dllm_struct_size(int which) {
         case 6: return sizeof(dllm_loop_info_t);
         case 7: return sizeof(dllm_vocab_shard);
         case 8: return sizeof(dllm_loop_control);
+        case 9: return sizeof(dllm_logprobs_args);
+        case 10: return sizeof(dllm_kv4_cache);
+        case 11: return sizeof(dllm_kv4_write_args);
+        case 12: return sizeof(dllm_kv4_attend_args);
+        case 13: return sizeof(dllm_kv4_evict_args);
         default: return 0;
     }
 }

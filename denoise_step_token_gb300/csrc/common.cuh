@@ -37,6 +37,12 @@ int* error_word_ptr();
 // SM count of the current device (cached per device).
 int sm_count();
 
+// Join counters at the start of the workspaces of dllm_logprobs and
+// dllm_kv4_attend, zero between calls.  Always as many, so that no call's data
+// lands on another's counters, whatever their shapes: one workspace may serve
+// both.
+constexpr int kJoinCounters = 2048;
+
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // ---------------------------------------------------------------------------

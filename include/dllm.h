@@ -56,6 +56,7 @@ extern "C" {
 #define DLLM_DEVERR_ROW_WIDTH 2   /* dllm_pack: p + (b + 1) * L > W for a row */
 #define DLLM_DEVERR_BLOCK_INDEX 3 /* dllm_advance: block index outside [0, K) or output row too short */
 #define DLLM_DEVERR_LOGITS_ROWS 4 /* dllm_step_compact: more masked positions than logits rows */
+#define DLLM_DEVERR_PAGE 5        /* dllm_kv4_*: a page number, length or position outside the cache */
 
 #define DLLM_MAX_L 1024
 #define DLLM_NUM_FEATURES 6
@@ -75,7 +76,10 @@ int dllm_last_cuda_error(const char** name);
 /* sizeof() of the argument structs below, for binding self-checks:
  * which = 0 dllm_step_args, 1 dllm_pack_args, 2 dllm_compact_args,
  * 3 dllm_advance_args, 4 dllm_refill_args, 5 dllm_loop_config,
- * 6 dllm_loop_info_t, 7 dllm_vocab_shard.  Returns 0 for an unknown `which`. */
+ * 6 dllm_loop_info_t, 7 dllm_vocab_shard, 8 dllm_loop_control,
+ * 9 dllm_logprobs_args, 10 dllm_kv4_cache, 11 dllm_kv4_write_args,
+ * 12 dllm_kv4_attend_args, 13 dllm_kv4_evict_args.  Returns 0 for an unknown
+ * `which`. */
 size_t dllm_struct_size(int which);
 
 /* Fault injection for tests of the status plumbing (host only; nothing
@@ -712,6 +716,192 @@ int dllm_loop_set_control(dllm_loop* loop, const dllm_loop_control* control);
  * thr (host, room for the loop's capacity).  Without control they are the
  * requests' own thresholds. */
 int dllm_loop_thresholds(const dllm_loop* loop, float* thr, int32_t* n);
+
+/* ======================================================================
+ * Operators around the step: the report of log probabilities over the
+ * step's logits, and a paged cache of keys and values in 4 bits (write,
+ * attention, eviction).  A block's denoise steps overwrite the block's own
+ * cache slots (FDFO page, section "工程设计四": a block that is not done keeps
+ * its slots), attend over the cache, and step.
+ * ====================================================================== */
+
+/* Log probabilities of given tokens, entropy and the best alternatives.  For
+ * entry i over x = logits row r (r = rows[i], or i when rows is NULL), with
+ * m = max_v x_v and z = sum_v exp(x_v - m):
+ *   logprob[i]  = x_t - m - ln z for t = tokens[i];
+ *   entropy[i]  = ln z - (sum_v exp(x_v - m) (x_v - m)) / z, terms of
+ *                 probability 0 counting 0;
+ *   top_ids[i][0..top) / top_logprobs[i][0..top): the tokens of largest
+ *                 value, largest first, ties to the lowest token (-0 == +0),
+ *                 and their log probabilities; -1 / NaN past the V tokens.
+ * A token outside [0, V) (-1: none asked) gets logprob NaN.  A row without a
+ * finite maximum (all -inf, or holding +inf or NaN) gets NaN everywhere and
+ * top_ids -1; so does an entry whose row is outside [0, logits_rows).  Sums
+ * are held in 32 bits and combined in a fixed order, so equal calls give
+ * equal bits (the split of a row, and with it the last bits, depend on N).
+ * Serves reports of sampled blocks: no gradient. */
+#define DLLM_MAX_TOP 32
+#define DLLM_DTYPE_BF16 0
+#define DLLM_DTYPE_F32 1
+typedef struct dllm_logprobs_args {
+    int32_t N;                  /* entries (>= 0) */
+    int32_t V;                  /* vocabulary size (>= 1) */
+    int32_t top;                /* alternatives, 0..DLLM_MAX_TOP */
+    int32_t dtype;              /* of the logits: DLLM_DTYPE_BF16 or DLLM_DTYPE_F32 */
+    int64_t ldv;                /* row stride in elements: >= V, a multiple of 16 bytes */
+    int64_t logits_rows;        /* rows of logits (>= 0) */
+    const void* logits;         /* device [logits_rows][ldv], 16-byte aligned */
+    const int32_t* rows;        /* device [N] row of each entry, or NULL: entry i is row i */
+    const int32_t* tokens;      /* device [N], or NULL with logprob NULL */
+    float* logprob;             /* device [N] out, or NULL with tokens NULL */
+    float* entropy;             /* device [N] out, or NULL */
+    int32_t* top_ids;           /* device [N][top] out (NULL when top is 0) */
+    float* top_logprobs;        /* device [N][top] out (NULL when top is 0) */
+    void* workspace;            /* device, >= dllm_logprobs_workspace_size() bytes, 256-byte aligned,
+                                   zero-filled before first use; every completed call leaves it ready
+                                   for the next; calls sharing it must be ordered on one stream */
+    size_t workspace_bytes;
+} dllm_logprobs_args;
+
+/* Workspace bytes for any call with at most N entries, this V and this top
+ * (0 if invalid). */
+size_t dllm_logprobs_workspace_size(int32_t N, int32_t V, int32_t top);
+
+/* Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_WORKSPACE, DLLM_ERR_CUDA. */
+int dllm_logprobs(const dllm_logprobs_args* args, void* stream);
+
+/* The 4-bit cache.  A pool of n_pages pages, each holding page_size tokens of
+ * every key/value head; request b's token j is slot j % page_size of page
+ * table[b][j / page_size].  One head's part of a page is contiguous,
+ *   key codes [page_size][D/2], key parameters [page_size][D/32] (uint16),
+ *   value codes [page_size][D/2], value parameters [page_size][D/32],
+ * i.e. dllm_kv4_page_bytes() = page_size * (D + D/8) bytes, and a page holds
+ * its heads one after the other.
+ * A group of 32 channels has a step s (4 significant bits, 2^-18 <= s <= 768)
+ * and a zero point z in [0, 15]; code u stands for s * (u - z).  8 significant
+ * bits hold that value exactly (bf16 and fp16 alike).  Parameter: the fp16
+ * pattern of 16 s (its low 7 bits are zero) with z in its low 4 bits; a NaN
+ * pattern makes the whole group NaN.  A 32-bit word of codes holds 8
+ * channels: channels 2i and 2i + 1 are bits [4i, 4i + 4) and
+ * [16 + 4i, 16 + 4i + 4).
+ * Each entry point takes the cache as: */
+#define DLLM_KV4_GROUP 32
+typedef struct dllm_kv4_cache {
+    int32_t n_pages;            /* >= 1 */
+    int32_t heads;              /* key/value heads, >= 1 */
+    int32_t page_size;          /* 16, 32, 64, 128 or 256 */
+    int32_t head_dim;           /* D: 64 or 128 */
+    int32_t B;                  /* requests (>= 0) */
+    int32_t max_pages;          /* table entries per request (>= 1) */
+    uint8_t* pages;             /* device [n_pages][heads][page bytes], 16-byte aligned */
+    const int32_t* table;       /* device [B][max_pages]; entries past a request's tokens are not read */
+} dllm_kv4_cache;
+/* A table entry outside [0, n_pages), or a length or position beyond
+ * max_pages * page_size, sets DLLM_DEVERR_PAGE; no memory outside the pool is
+ * touched and that request's results are unspecified. */
+
+/* Bytes of one head's part of a page (0 for an unsupported page_size or D). */
+size_t dllm_kv4_page_bytes(int32_t page_size, int32_t head_dim);
+
+/* Write keys and values into the cache.  For request b and column c with
+ * first[b] <= c < first[b] + count[b], the 16-bit rows k / v[b][c][h] become
+ * the codes of token pos[b] + c - first[b] of head h (what those slots held is
+ * overwritten).  Per group of 32 channels, with the range widened to hold 0:
+ *   s = (max - min) / 15 rounded up to 4 significant bits, at least 2^-18;
+ *   z = rint(-min / s), at most 15;  then s = min(s, 768);
+ *   u = clamp(rint(x / s) + z, 0, 15)
+ * (32-bit arithmetic, rint to even; what 768 is too small for saturates).  A
+ * group holding an infinity or a NaN is written as NaN (codes 0).  k_out / v_out receive what the codes stand for, so that a
+ * forward over the prompt may use the values later steps will see.
+ *   - strides in elements, multiples of 8, channels contiguous, base 16-byte
+ *     aligned; k_out / v_out are contiguous [B][W][heads][D] (columns not
+ *     written are left as they were).
+ * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+typedef struct dllm_kv4_write_args {
+    dllm_kv4_cache cache;
+    int32_t W;                  /* columns (>= 0) */
+    int32_t pad0;
+    const uint16_t* k;          /* device bf16 [B][W][heads][D] by the strides below */
+    const uint16_t* v;
+    int64_t k_stride[3];        /* request, column, head */
+    int64_t v_stride[3];
+    const int32_t* pos;         /* device [B] cache position of the first written column (>= 0) */
+    const int32_t* first;       /* device [B], or NULL: column 0 */
+    const int32_t* count;       /* device [B], or NULL: all columns from first */
+    uint16_t* k_out;            /* device bf16 [B][W][heads][D], or NULL */
+    uint16_t* v_out;
+} dllm_kv4_write_args;
+
+int dllm_kv4_write(const dllm_kv4_write_args* args, void* stream);
+
+/* Attention of a block of L query positions per request over the cache.  For
+ * request b, query head h (key/value head h / (q_heads / heads)) and position
+ * i, over the tokens j < lens[b]:
+ *   a_j = scale * q . k_j;  lse = ln sum_j exp(a_j);
+ *   out = sum_j exp(a_j - lse) v_j
+ * (every position sees every cached token: a block attends to its prefix and,
+ * once written, to itself in both directions).  With lens[b] <= 0, out is 0
+ * and lse -inf.  With weights, each cached token also receives what its head's
+ * queries gave it:
+ *   weights[page][g][slot] = prior[page][g][slot] + sum over the L positions
+ *     and the q_heads / heads query heads of g of exp(a_j - lse)
+ * (prior NULL: 0; prior may be weights; slots past lens[b] are not written;
+ * no atomics, so equal calls give equal bits).  Pages shared between requests
+ * must not be given weights in one call.
+ * Keys and values enter the products exactly; queries are scaled by a power
+ * of two per row into fp16 range; softmax weights are rounded to fp16 for the
+ * product with the values; sums and statistics are held in 32 bits.
+ * lens[b] may be anything up to max_pages * page_size.
+ * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_WORKSPACE,
+ * DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+typedef struct dllm_kv4_attend_args {
+    dllm_kv4_cache cache;
+    int32_t L;                  /* query positions per request, 1..DLLM_MAX_L */
+    int32_t q_heads;            /* a multiple of cache.heads */
+    float scale;                /* finite */
+    int32_t pad0;
+    const uint16_t* q;          /* device bf16 [B][L][q_heads][D] by the strides; 16-byte aligned */
+    int64_t q_stride[3];        /* request, position, head; multiples of 8, channels contiguous */
+    const int32_t* lens;        /* device [B] */
+    uint16_t* out;              /* device bf16 [B][L][q_heads][D], contiguous, 16-byte aligned */
+    float* lse;                 /* device [B][L][q_heads] out, or NULL without weights */
+    const float* prior;         /* device [n_pages][heads][page_size], or NULL */
+    float* weights;             /* device [n_pages][heads][page_size] out, or NULL */
+    void* workspace;            /* as dllm_logprobs_args: zero-filled before first use */
+    size_t workspace_bytes;
+} dllm_kv4_attend_args;
+
+/* Workspace bytes (0 if invalid). */
+size_t dllm_kv4_attend_workspace_size(const dllm_kv4_cache* cache, int32_t L, int32_t q_heads);
+
+int dllm_kv4_attend(const dllm_kv4_attend_args* args, void* stream);
+
+/* Evict a cache's least attended tokens: for request b and head h, the last
+ * min(recent, k) tokens and the largest weights among the others, ties to the
+ * lowest token, k = min(keep[b], lens[b]) tokens in all (0 when either is
+ * negative), move in their order to tokens 0..k-1 of the pages of
+ * dst_table[b], with their weights.  A NaN weight counts as the smallest.
+ *   dst_lens[b] = k;  src[b][h][i] = the token that became token i, -1 for
+ *   i >= k.
+ * The destination pages must be in the pool, used by no other request, and
+ * not among the source pages: the caller owns both and frees the source pages
+ * after the call.  k beyond dst_max_pages * page_size sets DLLM_DEVERR_PAGE
+ * and keeps that many.  cache.table, lens, keep and the source pages are not
+ * changed.  dst_lens must not alias lens or keep.
+ * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+typedef struct dllm_kv4_evict_args {
+    dllm_kv4_cache cache;
+    int32_t recent;             /* >= 0 */
+    int32_t dst_max_pages;      /* >= 1 */
+    const int32_t* lens;        /* device [B] */
+    const int32_t* keep;        /* device [B] */
+    float* weights;             /* device [n_pages][heads][page_size]: read at the source, written at the destination */
+    const int32_t* dst_table;   /* device [B][dst_max_pages] */
+    int32_t* dst_lens;          /* device [B] out */
+    int32_t* src;               /* device [B][heads][dst_max_pages * page_size] out */
+} dllm_kv4_evict_args;
+
+int dllm_kv4_evict(const dllm_kv4_evict_args* args, void* stream);
 
 #ifdef __cplusplus
 }
