@@ -20,40 +20,10 @@
 
 #include <algorithm>
 
-#include "kv4_mma.cuh"
+#include "kv4_attend.cuh"
 
 namespace dllm {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kBelow = 7.0f;    // the offset sits this far below the maximum it was set from
-constexpr float kAbove = 15.0f;   // and moves when a score passes it by more than this
-
-struct AttendParams {
-    Kv4 C;
-    QueryRows Q;
-    int q_heads, tiles, splits;   // 16-row tiles per key/value head
-    float scale2;                 // scale * log2 e
-    const int* lens;
-    uint16_t* out;
-    float* lse;
-    const float* prior;
-    float* weights;
-    int* counters;     // zero between calls
-    float* partial;    // [unit][split][16 * (D + 2)]
-};
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
 
 // ---------------------------------------------------------------------------
 // Few rows: 16 rows per CTA, four warps with 16 tokens at a time
@@ -286,8 +256,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const _
     }
     const int r = tile * 16 + row;
     if (r >= P.Q.rows) return;
-    const int i = r / P.Q.group;
-    const long long at = ((long long)b * P.Q.L + i) * P.q_heads + head * P.Q.group + (r - i * P.Q.group);
+    const long long at = P.row_at(b, head, r);
     if (part == 0 && P.lse) P.lse[at] = n > 0 ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     const float inv = n > 0 ? 1.0f / ll : 0.0f;
     uint4* dst = reinterpret_cast<uint4*>(P.out + at * D + part * kNt);
@@ -369,9 +338,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv4_weights_kernel(const __
             if (lane == 0) {
                 float2 v = make_float2(0.0f, INFINITY);   // a row past the end gives 2^(0 - inf) = 0
                 if (r < P.Q.rows) {
-                    const int i = r / P.Q.group;
-                    const long long at = ((long long)b * P.Q.L + i) * P.q_heads + head * P.Q.group + (r - i * P.Q.group);
-                    v = make_float2(P.scale2 * up, P.lse[at] * kLog2e);
+                    v = make_float2(P.scale2 * up, P.lse[P.row_at(b, head, r)] * kLog2e);
                 }
                 s_row[rr] = v;
             }
@@ -414,7 +381,8 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv4_weights_kernel(const __
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int kMaxSlots = 8192;   // splits of all units (request, head, tile) in a call
+constexpr int kMaxSlots = 4096;   // splits of all units (request, head, tile) in a call
+constexpr int kFewRows = 32;      // up to this many rows per key/value head: kv4_attend_rows_kernel
 
 // Splits of a unit's tokens: enough that every SM has its three resident CTAs
 // a few times over, none under 256 tokens.
@@ -424,6 +392,13 @@ inline int pick_splits(long long units, int max_tokens, int sms) {
     s = std::min<long long>(s, (max_tokens + 255) / 256);
     s = std::min<long long>(s, kMaxSlots / units);
     return (int)std::max<long long>(std::min<long long>(s, 64), 1);
+}
+
+// Blocks of rows of a key/value head, and the items a plan may hold: every unit
+// once, and a piece more for every CTA.
+inline int row_blocks(int rows) { return (rows + kTileRows - 1) / kTileRows; }
+inline size_t max_items(const dllm_kv4_cache& c, int rows) {
+    return (size_t(std::max(c.B, 1)) * c.heads * row_blocks(rows) + kMaxCtas + 7) & ~size_t(7);
 }
 
 inline int check_rows(const dllm_kv4_cache& c, int L, int q_heads) {
@@ -440,7 +415,11 @@ using namespace dllm;
 extern "C" size_t dllm_kv4_attend_workspace_size(const dllm_kv4_cache* c, int32_t L, int32_t q_heads) {
     if (!c || c->heads < 1 || dllm_kv4_page_bytes(c->page_size, c->head_dim) == 0) return 0;
     if (check_rows(*c, L, q_heads) != DLLM_OK) return 0;
-    return size_t(kJoinCounters) * 4 + size_t(kMaxSlots) * 16 * (c->head_dim + 2) * 4;
+    const int rows = L * (q_heads / c->heads);
+    size_t n = size_t(kJoinCounters) * 4;
+    if (rows <= kFewRows) return n + size_t(kMaxSlots) * 16 * (c->head_dim + 2) * 4;
+    n += sizeof(TilePlan) + max_items(*c, rows) * sizeof(TileItem);
+    return n + size_t(2 * kMaxCtas) * kTileRows * (c->head_dim + 2) * 4;
 }
 
 extern "C" int dllm_kv4_attend(const dllm_kv4_attend_args* a, void* stream) {
@@ -467,19 +446,33 @@ extern "C" int dllm_kv4_attend(const dllm_kv4_attend_args* a, void* stream) {
     if (rc != DLLM_OK) return rc;
     P.Q = QueryRows{a->q, a->q_stride[0], a->q_stride[1], a->q_stride[2], a->L, group, a->L * group};
     P.q_heads = a->q_heads;
-    P.tiles = (P.Q.rows + 15) / 16;
-    P.splits = pick_splits((long long)B * H * P.tiles, P.C.max_tokens, sms);
     P.scale2 = a->scale * kLog2e;
     P.lens = a->lens;
     P.out = a->out;
     P.lse = a->lse;
     P.prior = a->prior;
     P.weights = a->weights;
-    P.counters = static_cast<int*>(a->workspace);
-    P.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(a->workspace) + size_t(kJoinCounters) * 4);
+    P.tiles = (P.Q.rows + 15) / 16;
+    P.splits = pick_splits((long long)B * H * P.tiles, P.C.max_tokens, sms);
+    unsigned char* ws = static_cast<unsigned char*>(a->workspace);
+    P.counters = reinterpret_cast<int*>(ws);
+    ws += size_t(kJoinCounters) * 4;
+    P.row_blocks = row_blocks(P.Q.rows);
+    P.block_rows = (P.Q.rows + P.row_blocks - 1) / P.row_blocks;
+    P.ctas = std::min(sms, kMaxCtas);
+    P.plan = reinterpret_cast<TilePlan*>(ws);
+    P.items = reinterpret_cast<TileItem*>(ws + sizeof(TilePlan));
     cudaStream_t s = as_stream(stream);
-    DLLM_CUDA_TRY(launch_dependent(D == 128 ? kv4_attend_rows_kernel<128> : kv4_attend_rows_kernel<64>,
-                                   dim3(P.splits, H * P.tiles, B), dim3(kRowWarps * 32), 0, s, P));
+    if (P.Q.rows <= kFewRows) {
+        P.partial = reinterpret_cast<float*>(ws);
+        DLLM_CUDA_TRY(launch_dependent(D == 128 ? kv4_attend_rows_kernel<128> : kv4_attend_rows_kernel<64>,
+                                       dim3(P.splits, H * P.tiles, B), dim3(kRowWarps * 32), 0, s, P));
+    } else {
+        P.partial = reinterpret_cast<float*>(ws + sizeof(TilePlan) + max_items(a->cache, P.Q.rows) * sizeof(TileItem));
+        rc = launch_attend_tiles(P, D, s);
+        if (rc != DLLM_OK) return rc;
+    }
+    if (a->weights && P.Q.rows > kFewRows) return launch_weight_tiles(P, D, s);
     if (a->weights) {
         const unsigned gx = (P.C.max_tokens + kWeightWarps * 32 - 1) / (kWeightWarps * 32);
         DLLM_CUDA_TRY(launch_dependent(D == 128 ? kv4_weights_kernel<128> : kv4_weights_kernel<64>, dim3(gx, H, B),

@@ -523,3 +523,24 @@ def test_refusals(dllm):
     dllm.kv4_write(k[:0], k[:0], pages, none, empty)
     assert dllm.kv4_evict(pages, weights, none, empty, empty, none)["lens"].numel() == 0
     assert dllm.get_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("L,H,heads", [(32, 2, 2), (32, 7, 1), (40, 8, 1), (1, 4, 1)])
+def test_attend_many_short_requests(dllm, L, H, heads):
+    """Hundreds of requests of one or two tiles, empty ones among them: every
+    CTA runs through several, its warps items apart."""
+    rng = np.random.default_rng(30)
+    lens = rng.choice([0, 1, 100, 128, 129, 250, 257], 700)
+    lens[:200] = rng.choice([0, 128], 200)
+    cache = Cache(rng, lens, heads, 64, 64, extra=0)
+    check_attend(dllm, cache, rng.standard_normal((700, L, H, 64)), weights=True)
+
+
+def test_attend_one_long_among_short(dllm):
+    """One request far longer than the others is cut over the CTAs."""
+    rng = np.random.default_rng(31)
+    lens = [64] * 40 + [20000] + [300] * 3
+    cache = Cache(rng, lens, 1, 64, 256, extra=0)
+    check_attend(dllm, cache, rng.standard_normal((44, 33, 4, 64)), weights=True)
+    check_attend(dllm, cache, rng.standard_normal((44, 33, 1, 64)), weights=True)
+    check_attend(dllm, cache, rng.standard_normal((44, 1, 4, 64)), weights=True)
