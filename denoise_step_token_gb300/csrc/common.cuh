@@ -186,6 +186,23 @@ __device__ __forceinline__ unsigned long long f32x2_splat(float x) {
     return (u << 32) | u;
 }
 
+__device__ __forceinline__ unsigned long long f32x2_add(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_mul(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_fma(unsigned long long a, unsigned long long b,
+                                                        unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // acc += (2^(lo * s + n), 2^(hi * s + n)) for the two bf16 values of `w`
 // (lo = the low half, widened exactly by moving it to the top 16 bits; hi =
 // the high half with the low 16 bits cleared).  s and n are f32x2 pairs.

@@ -1,14 +1,15 @@
 // dllm_logprobs: log probabilities of given tokens, entropy and the best
 // alternatives of logits rows, in one pass over each row.
 //
-// Mathematics.  With m = max x, z = sum exp(x - m) and t = sum exp(x - m)(x - m):
-//   log p_v = x_v - m - ln z,   entropy = ln z - t / z.
-// m, z and t are kept running: moving from m to m' >= m scales z by
-// f = exp(m - m') and takes t to f (t + z (m - m')).
+// Mathematics, in base 2 (c = log2 e).  With m = max x, y_v = c x_v - c m,
+// z = sum 2^y and t = sum 2^y y:
+//   log p_v = ln 2 (y_v - log2 z),   entropy = ln 2 (log2 z - t / z).
+// m, z and t are kept running: moving from m to m' >= m with d = c m - c m'
+// scales z by f = 2^d and takes t to f (t + z d).
 //
-// What bounds it: reading the rows (one FMA-class operation or so per value
-// and 1 exp, well under the issue rate at 2 bytes a value), or, for a row or
-// two, the launch and the joins.
+// What bounds it: reading the rows (4 instructions a value at 2 bytes a value,
+// about half of what an SM can issue while its share of memory arrives), or,
+// for a row or two, the launch and the joins.
 //
 // Split.  A row is cut into `pieces` runs of whole rounds (a round: 256
 // threads x 64 bytes); one CTA reduces one piece with 16-byte loads straight
@@ -19,12 +20,15 @@
 //
 // Best alternatives.  A value and its token make one 64-bit key (the value's
 // order-preserving bits above the inverted token), so all keys differ and
-// larger keys come first.  Each piece keeps a candidate list in shared memory
-// and a threshold below which nothing can be among its best `top`: the first
-// round takes the top-th largest of the threads' own maxima (at least `top`
-// values reach it, and only `top` threads can hold such values, so the list
-// cannot overflow); later rounds append what exceeds the threshold and sort
-// the list down to `top` by counting when it fills.
+// larger keys come first.  The streaming threads only compare their round's
+// maximum with a floor and note (round, thread) in a list when it passes.  After
+// rounds 1, 2, 4, 8, ... the noted values are read again (from L2), those above
+// the floor sorted among the best so far by counting, and the floor rises to
+// the top-th of them; each stage notes about `top` threads.  The first floor: in
+// each full warp the q-th largest of its lanes' maxima, q warps >= top, and the
+// least of those over the warps; at least `top` values of the round reach it.
+// Rows that overfill the lists (sorted ones, many equal values) take a radix
+// selection over the piece instead.
 
 #include <math.h>
 #include <stdint.h>
@@ -43,7 +47,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kVec = 4;              // 16-byte loads per thread and round
 constexpr int kMaxPieces = 32;
 constexpr int kMaxSlots = 4096;      // pieces of cut rows in all
-constexpr int kCap = 1024 + 64;      // candidates: at most 32 values of each of DLLM_MAX_TOP threads, and the kept
+constexpr int kCap = 1024;           // candidate keys of a stage, the best so far among them
+constexpr int kHits = 512;           // noted threads of a stage
+constexpr float kPlain = 16384.0f;   // maxima up to this size take the packed loop
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -90,14 +96,26 @@ struct Sums {
     float m, z, t;
 };
 
+// c a - c b as the sums hold it (c m is rounded once, the same everywhere).
+__device__ __forceinline__ float diff2(float a, float b) {
+    return fabsf(b) <= kPlain && fabsf(a) <= kPlain ? __fsub_rn(__fmul_rn(a, kLog2e), __fmul_rn(b, kLog2e))
+                                                    : (a - b) * kLog2e;
+}
+// ln p of one value, lz = log2 z: by the y the sums were formed with where c x
+// is sure to be finite.
+__device__ __forceinline__ float log_prob(float x, float m, float lz) {
+    if (fabsf(m) <= kPlain && fabsf(x) <= kPlain) return (fmaf(x, kLog2e, -__fmul_rn(m, kLog2e)) - lz) * kLn2;
+    return (x - m) - lz * kLn2;
+}
+
 // (a, then b): sums over both ranges.
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
     Sums r;
     r.m = max_nan(a.m, b.m);
     if (r.m == -INFINITY) return Sums{-INFINITY, 0.0f, 0.0f};
     // a side without a finite value has z = 0 and drops out
-    const float da = fmaxf(a.m - r.m, -1e4f), db = fmaxf(b.m - r.m, -1e4f);
-    const float fa = exp2f(da * kLog2e), fb = exp2f(db * kLog2e);
+    const float da = fmaxf(diff2(a.m, r.m), -1e4f), db = fmaxf(diff2(b.m, r.m), -1e4f);
+    const float fa = exp2f(da), fb = exp2f(db);
     r.z = a.z * fa + b.z * fb;
     r.t = fa * (a.t + a.z * da) + fb * (b.t + b.z * db);
     return r;
@@ -185,7 +203,7 @@ __device__ __forceinline__ float round_max(const uint4 (&q)[kVec]) {
 // Sort `n` keys of `list` (n <= kCap, every thread calls) by counting; the
 // largest min(n, top) end up first, largest first.  Returns that count.
 __device__ __forceinline__ int keep_best(u64* list, int n, int top) {
-    constexpr int kEach = (kCap + kThreads - 1) / kThreads;
+    constexpr int kEach = kCap / kThreads;
     u64 mine[kEach];
     int rank[kEach];
 #pragma unroll
@@ -209,55 +227,195 @@ __device__ __forceinline__ int keep_best(u64* list, int n, int top) {
 
 struct Shared {
     u64 list[kCap];
-    u64 maxes[kThreads];
+    int hits[kHits];
+    int hist[256];
     Sums part[kWarps];
-    u64 bound;
-    int count, last;
+    uint32_t floor;   // of the first round
+    uint32_t prefix;
+    int count, n_hits, over, need, last;
 };
 
-// Append this thread's values of the round that have keys >= bound.
 template <typename T>
-__device__ __forceinline__ void append(Shared& sh, const uint4 (&q)[kVec], int v0, int V, u64 bound) {
-    constexpr int per = Round<T>::kPer;
-    const float low = key_floor(bound);
+__device__ __forceinline__ float load_value(const T* row, int v) {
+    if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)__ldg(row + v) << 16);
+    else return __ldg(row + v);
+}
+
+// Read the noted threads' values again and append the keys above `above`; then
+// keep the best.  Every thread calls; returns how many are kept, sorted.
+template <typename T>
+__device__ __forceinline__ int take_hits(Shared& sh, const T* row, int V, int top, int kept, u64 above) {
+    constexpr int per = Round<T>::kPer, values = kVec * per;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int hits = min(sh.n_hits, kHits);
+    if (threadIdx.x == 0) sh.count = kept;
+    __syncthreads();
+    const float low = key_floor(above);
+    constexpr int kAtOnce = 4;
+    for (int h0 = warp * kAtOnce; h0 < hits; h0 += kWarps * kAtOnce) {
+        float x[kAtOnce];
+        int v[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int h = h0 + u < hits ? sh.hits[h0 + u] : -1;
+            v[u] = (h / kThreads) * (kThreads * values) + ((lane / per) * kThreads + h % kThreads) * per + lane % per;
+            x[u] = -INFINITY;
+            if (h >= 0 && lane < values && v[u] < V) x[u] = load_value(row, v[u]);
+            else v[u] = -1;
+        }
 #pragma unroll
-        for (int k = 0; k < per; ++k) {
-            const float x = Round<T>::get(q[i], k);
-            if (x >= low) {
-                const int v = v0 + (i * kThreads + (int)threadIdx.x) * per + k;
-                const u64 key = make_key(x, v);
-                if (v < V && key >= bound) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kCap) sh.list[at] = key;
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (v[u] < 0 || !(x[u] >= low)) continue;
+            const u64 key = make_key(x[u], v[u]);
+            if (key > above) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kCap) sh.list[at] = key;
+            }
+        }
+    }
+    __syncthreads();
+    const int n = sh.count;
+    if (n > kCap || sh.n_hits > kHits) {   // too many to sort: the piece is selected anew at its end
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sh.over = 1;
+            sh.n_hits = 0;
+        }
+        __syncthreads();
+        return kept;
+    }
+    const int k = keep_best(sh.list, n, top);
+    if (threadIdx.x == 0) sh.n_hits = 0;
+    __syncthreads();
+    return k;
+}
+
+// The best `top` of values [v0, v1) by radix selection, into the list, sorted.
+template <typename T>
+__device__ __noinline__ int select_slow(Shared& sh, const T* row, int v0, int v1, int top) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = v1 - v0;
+    if (tid == 0) sh.count = 0;
+    if (n <= top) {
+        __syncthreads();
+        for (int v = v0 + tid; v < v1; v += kThreads) sh.list[v - v0] = make_key(load_value(row, v), v);
+        __syncthreads();
+        return keep_best(sh.list, n, top);
+    }
+    uint32_t prefix = 0;
+    int need = top;
+    for (int shift = 24; shift >= (sizeof(T) == 2 ? 16 : 0); shift -= 8) {
+        sh.hist[tid] = 0;
+        __syncthreads();
+        for (int v = v0 + tid; v < v1; v += kThreads) {
+            const uint32_t k = ordered(load_value(row, v));
+            if (shift == 24 || ((k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&sh.hist[(k >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            int left = need, bin = 255;
+            while (bin > 0 && sh.hist[bin] < left) left -= sh.hist[bin--];
+            sh.prefix = prefix | ((uint32_t)bin << shift);
+            sh.need = left;
+        }
+        __syncthreads();
+        prefix = sh.prefix;
+        need = sh.need;
+        __syncthreads();
+    }
+    // of the values with this prefix (bf16: equal ones) the first `need` tokens
+    constexpr uint32_t kBits = sizeof(T) == 2 ? 0xffff0000u : 0xffffffffu;
+    int before = 0;
+    for (int w0 = v0; w0 < v1; w0 += kThreads) {
+        const int v = w0 + tid;
+        const float x = v < v1 ? load_value(row, v) : 0.0f;
+        const uint32_t k = ordered(x) & kBits;
+        const bool eq = v < v1 && k == prefix;
+        const unsigned bal = __ballot_sync(0xffffffffu, eq);
+        if (lane == 0) sh.hist[warp] = __popc(bal);
+        __syncthreads();
+        int here = before;
+        for (int w = 0; w < kWarps; ++w) {
+            here += w < warp ? sh.hist[w] : 0;
+            before += sh.hist[w];
+        }
+        if (v < v1 && (k > prefix || (eq && here + __popc(bal & ((1u << lane) - 1u)) < need)))
+            sh.list[atomicAdd(&sh.count, 1)] = make_key(x, v);   // `top` in all
+        __syncthreads();
+    }
+    return keep_best(sh.list, sh.count, top);
+}
+
+// z and t of a round's values above the running m (m is at least their maximum).
+template <typename T>
+__device__ __forceinline__ void round_sums(const uint4 (&q)[kVec], float m, u64& z2, u64& t2) {
+    if (fabsf(m) <= kPlain) {
+        // values under -2 kPlain are 2^(-20000) = 0 all the same: held there, -inf adds 0 to both sums
+        const u64 c2 = f32x2_splat(kLog2e), n2 = f32x2_splat(-__fmul_rn(m, kLog2e));
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t x = bf16x2_max(w[k], 0xc700c700u);
+                    asm("{\n\t.reg .b32 l, h;\n\t.reg .b64 y, p;\n\t"
+                        "prmt.b32 l, %2, 0, 0x1044;\n\t"
+                        "and.b32 h, %2, 0xffff0000;\n\t"
+                        "mov.b64 y, {l, h};\n\t"
+                        "fma.rn.f32x2 y, y, %3, %4;\n\t"
+                        "mov.b64 {l, h}, y;\n\t"
+                        "ex2.approx.ftz.f32 l, l;\n\t"
+                        "ex2.approx.ftz.f32 h, h;\n\t"
+                        "mov.b64 p, {l, h};\n\t"
+                        "add.rn.f32x2 %0, %0, p;\n\t"
+                        "fma.rn.f32x2 %1, p, y, %1;\n\t}"
+                        : "+l"(z2), "+l"(t2)
+                        : "r"(x), "l"(c2), "l"(n2));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const float l = fmaxf(__uint_as_float(w[k]), -2 * kPlain), h = fmaxf(__uint_as_float(w[k + 1]), -2 * kPlain);
+                    asm("{\n\t.reg .b32 l, h;\n\t.reg .b64 y, p;\n\t"
+                        "mov.b64 y, {%2, %3};\n\t"
+                        "fma.rn.f32x2 y, y, %4, %5;\n\t"
+                        "mov.b64 {l, h}, y;\n\t"
+                        "ex2.approx.ftz.f32 l, l;\n\t"
+                        "ex2.approx.ftz.f32 h, h;\n\t"
+                        "mov.b64 p, {l, h};\n\t"
+                        "add.rn.f32x2 %0, %0, p;\n\t"
+                        "fma.rn.f32x2 %1, p, y, %1;\n\t}"
+                        : "+l"(z2), "+l"(t2)
+                        : "f"(l), "f"(h), "l"(c2), "l"(n2));
                 }
             }
         }
-}
-
-// The top-th largest of the threads' largest keys of the round (0 when fewer
-// threads have one): at least `top` keys of the round reach it.
-template <typename T>
-__device__ __forceinline__ u64 round_bound(Shared& sh, const uint4 (&q)[kVec], int v0, int V, int top) {
-    constexpr int per = Round<T>::kPer;
-    u64 best = 0;
+        return;
+    }
+    if (m == -INFINITY) return;   // nothing yet
+    float z = 0.0f, t = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < kVec * Round<T>::kPer; ++i) {
+        uint4 v = q[0];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+        for (int k = 1; k < kVec; ++k)
+            if (i / Round<T>::kPer == k) v = q[k];
+        const int e = i % Round<T>::kPer;
+        float x = Round<T>::get(v, 0);
 #pragma unroll
-        for (int k = 0; k < per; ++k) {
-            const int v = v0 + (i * kThreads + (int)threadIdx.x) * per + k;
-            const u64 key = make_key(Round<T>::get(q[i], k), v);
-            if (v < V && key > best) best = key;
-        }
-    sh.maxes[threadIdx.x] = best;
-    if (threadIdx.x == 0) sh.bound = 0;
-    __syncthreads();
-    int r = 0;
-    for (int j = 0; j < kThreads; ++j) r += sh.maxes[j] > best;
-    if (best && r == top - 1) sh.bound = best;   // keys differ: one thread at most
-    __syncthreads();
-    return sh.bound;
+        for (int k = 1; k < Round<T>::kPer; ++k)
+            if (e == k) x = Round<T>::get(v, k);
+        const float y = fmaxf((x - m) * kLog2e, -1e4f), p = ex2_approx(y);
+        z += p;
+        t = fmaf(p, y, t);
+    }
+    z2 = f32x2_add(z2, (u64)__float_as_uint(z));
+    t2 = f32x2_add(t2, (u64)__float_as_uint(t));
 }
 
 // Results of entry i from its row's sums and its sorted keys.
@@ -266,30 +424,23 @@ __device__ __forceinline__ void write_entry(const LogprobParams& P, int i, const
                                             const u64* list, int kept) {
     const float nan = __int_as_float(0x7fc00000);
     const bool ok = row && isfinite(s.m);   // z >= 1 then
-    const float lnz = ok ? logf(s.z) : nan;
+    const float lz = ok ? log2f(s.z) : nan;
     if (threadIdx.x == 0) {
-        if (P.entropy) P.entropy[i] = ok ? lnz - s.t / s.z : nan;
+        if (P.entropy) P.entropy[i] = ok ? (lz - s.t / s.z) * kLn2 : nan;
         if (P.logprob) {
             const int t = P.tokens[i];
-            float lp = nan;
-            if (ok && t >= 0 && t < P.V) {
-                float x;
-                if constexpr (sizeof(T) == 2) x = __uint_as_float((uint32_t)row[t] << 16);
-                else x = row[t];
-                lp = (x - s.m) - lnz;
-            }
-            P.logprob[i] = lp;
+            P.logprob[i] = ok && t >= 0 && t < P.V ? log_prob(load_value(row, t), s.m, lz) : nan;
         }
     }
     for (int k = threadIdx.x; k < P.top; k += kThreads) {
         const bool have = ok && k < kept;
         P.top_ids[(long long)i * P.top + k] = have ? key_token(list[k]) : -1;
-        P.top_logprobs[(long long)i * P.top + k] = have ? (key_value(list[k]) - s.m) - lnz : nan;
+        P.top_logprobs[(long long)i * P.top + k] = have ? log_prob(key_value(list[k]), s.m, lz) : nan;
     }
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_constant__ LogprobParams P) {
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const __grid_constant__ LogprobParams P) {
     __shared__ Shared sh;
     constexpr int per = Round<T>::kPer;
     constexpr int kRound = kThreads * kVec * per;
@@ -305,10 +456,18 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_const
     }
     const int first = (int)((long long)P.rounds * piece / P.pieces);
     const int end = (int)((long long)P.rounds * (piece + 1) / P.pieces);
-    float m = -INFINITY, z = 0.0f, t = 0.0f;
-    u64 bound = 0;
-    int kept = 0;
-    if (tid == 0) sh.count = 0;
+    float m = -INFINITY;
+    u64 z2 = 0, t2 = 0;
+    u64 above = 0;        // keys at or under it are not among the best
+    float low = INFINITY; // what a round's maximum must pass to be noted
+    int kept = 0, stage = 1;
+    if (kTop) {
+        if (tid == 0) {
+            sh.n_hits = sh.over = 0;
+            sh.floor = 0xffffffffu;
+        }
+        __syncthreads();
+    }
     uint4 q[kVec], nx[kVec];
     load_round<T>(nx, row, first * kRound, P.V);
     for (int rd = first; rd < end; ++rd) {
@@ -320,50 +479,59 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const __grid_const
         const float bm = round_max<T>(q);
         if (!(bm <= m)) {
             const float mn = max_nan(m, bm);
-            const float d = fmaxf(m - mn, -1e4f), f = ex2_approx(d * kLog2e);
-            t = f * (t + z * d);
-            z *= f;
+            const float d = fmaxf(diff2(m, mn), -1e4f), f = ex2_approx(d);
+            const u64 f2 = f32x2_splat(f);
+            t2 = f32x2_mul(f2, f32x2_fma(z2, f32x2_splat(d), t2));
+            z2 = f32x2_mul(z2, f2);
             m = mn;
         }
-        // x - m is held above -1e4 (its exp is 0 there): -inf contributes 0 to both sums
-#pragma unroll
-        for (int k = 0; k < kVec; ++k)
-#pragma unroll
-            for (int e = 0; e < per; ++e) {
-                const float d = fmaxf(Round<T>::get(q[k], e) - m, -1e4f);
-                const float p = ex2_approx(d * kLog2e);
-                z += p;
-                t = fmaf(p, d, t);
-            }
+        round_sums<T>(q, m, z2, t2);
         if constexpr (kTop) {
             if (rd == first) {
-                bound = round_bound<T>(sh, q, v0, P.V, P.top);
-                append<T>(sh, q, v0, P.V, bound);
-                __syncthreads();
-            } else {
-                const int before = sh.count;   // the same in every thread: the barrier below orders it
-                __syncthreads();
-                if (bm >= key_floor(bound)) append<T>(sh, q, v0, P.V, bound + 1);
-                __syncthreads();
-                if (sh.count > kCap) {
-                    // more than the list holds: drop this round's, raise the threshold, take the round again
-                    const int n = keep_best(sh.list, before, P.top);
-                    if (n == P.top) bound = max(bound, sh.list[n - 1]);
-                    if (tid == 0) sh.count = n;
-                    const u64 rb = round_bound<T>(sh, q, v0, P.V, P.top);
-                    append<T>(sh, q, v0, P.V, max(rb, bound + 1));
-                    __syncthreads();
+                // the first floor, by bits of the order-preserving key from the top (16 of them)
+                const int full = min(max(P.V - v0, 0) / (32 * per), kWarps);   // warps whose lanes all have values
+                const uint32_t key = ordered(bm);
+                uint32_t fl = 0;
+                if (warp < full) {
+                    const int want = (P.top + full - 1) / full;
+#pragma unroll 1
+                    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+                        const unsigned at = __ballot_sync(0xffffffffu, key >= (fl | bit));
+                        if (__popc(at) >= want) fl |= bit;
+                    }
+                    if (lane == 0) atomicMin(&sh.floor, fl);
                 }
-            }
-            const int n = sh.count;
-            if (n > 128 || rd + 1 == end) {
-                kept = keep_best(sh.list, n, P.top);
-                if (kept == P.top) bound = max(bound, sh.list[kept - 1]);
-                if (tid == 0) sh.count = kept;
                 __syncthreads();
+                fl = full > 0 ? sh.floor : 0;
+                above = fl ? ((u64)fl << 32) - 1 : 0;   // every key of a value at the floor passes
+                low = key_floor(above + 1);
+                if (bm >= low) {
+                    const int at = atomicAdd(&sh.n_hits, 1);
+                    if (at < kHits) sh.hits[at] = rd * kThreads + tid;
+                }
+            } else if (bm > low || above == 0) {
+                const int at = atomicAdd(&sh.n_hits, 1);
+                if (at < kHits) sh.hits[at] = rd * kThreads + tid;
+            }
+            if (rd - first + 1 == stage || rd + 1 == end) {
+                stage *= 2;
+                __syncthreads();
+                if (!sh.over) {
+                    kept = take_hits<T>(sh, row, P.V, P.top, kept, above);
+                    if (kept == P.top && !sh.over) {
+                        above = max(above, sh.list[kept - 1]);
+                        low = key_value(above);
+                    }
+                    __syncthreads();   // the list is read before a later stage appends
+                }
             }
         }
     }
+    if constexpr (kTop) {
+        if (sh.over) kept = select_slow<T>(sh, row, first * kRound, min(end * kRound, P.V), P.top);
+    }
+    const float z = __uint_as_float((uint32_t)z2) + __uint_as_float((uint32_t)(z2 >> 32));
+    const float t = __uint_as_float((uint32_t)t2) + __uint_as_float((uint32_t)(t2 >> 32));
     Sums s{m, z, t};
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
