@@ -186,6 +186,13 @@ __device__ __forceinline__ unsigned long long f32x2_splat(float x) {
     return (u << 32) | u;
 }
 
+__device__ __forceinline__ unsigned long long f32x2_pack(float lo, float hi) {
+    unsigned long long d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float f32x2_lo(unsigned long long a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float f32x2_hi(unsigned long long a) { return __uint_as_float((uint32_t)(a >> 32)); }
 __device__ __forceinline__ unsigned long long f32x2_add(unsigned long long a, unsigned long long b) {
     unsigned long long d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

@@ -7,28 +7,31 @@
 // m, z and t are kept running: moving from m to m' >= m with d = c m - c m'
 // scales z by f = 2^d and takes t to f (t + z d).
 //
-// What bounds it: reading the rows (4 instructions a value at 2 bytes a value,
-// about half of what an SM can issue while its share of memory arrives), or,
-// for a row or two, the launch and the joins.
+// What bounds it: reading the rows (about 4.5 instructions a value, under half
+// of what an SM can issue while its share of memory arrives), or, for a row or
+// two, the launch and the joins.
 //
-// Split.  A row is cut into `pieces` runs of whole rounds (a round: 256
-// threads x 64 bytes); one CTA reduces one piece with 16-byte loads straight
-// to registers, the next round's in flight, several CTAs per SM.  With one
-// piece per row it writes the results itself; otherwise it publishes its
-// triple and its best `top` keys, and the piece that arrives last joins them
-// in piece order.
+// Split.  All entries' rounds (a round: 256 threads x 64 bytes of a row) are one
+// stream, cut evenly over the CTAs, six per SM.  A fifth warp keeps up to four
+// rounds of its CTA in flight as bulk copies (8 KB each, 190 KB per SM: under
+// load a copy lands about 2.8 us after its issue, and with the next round's loads
+// in registers, 64 KB per SM, the stream ran at 4.4 TB/s).  A CTA writes the
+// entries that lie wholly in its share; what it has of the two others it
+// publishes (sums and best keys), and whichever CTA arrives last at an entry
+// joins the parts in stream order.
 //
 // Best alternatives.  A value and its token make one 64-bit key (the value's
 // order-preserving bits above the inverted token), so all keys differ and
 // larger keys come first.  The streaming threads only compare their round's
-// maximum with a floor and note (round, thread) in a list when it passes.  After
-// rounds 1, 2, 4, 8, ... the noted values are read again (from L2), those above
-// the floor sorted among the best so far by counting, and the floor rises to
-// the top-th of them; each stage notes about `top` threads.  The first floor: in
-// each full warp the q-th largest of its lanes' maxima, q warps >= top, and the
-// least of those over the warps; at least `top` values of the round reach it.
-// Rows that overfill the lists (sorted ones, many equal values) take a radix
-// selection over the piece instead.
+// maximum with a floor; a warp looks through the 32 values of a thread whose
+// maximum passes, one value per lane, while the round is in shared memory, and
+// appends the keys above the floor to a list.  After rounds 1, 4, 16, ... the list
+// is sorted by counting down to the best `top`, and the floor rises to the last
+// of them: about 3 `top` keys come while what was seen grows fourfold.  The
+// first floor: in each full warp the q-th largest of its lanes' maxima, q warps
+// >= top, and the least of those over the warps; at least `top` values of the
+// round reach it.  Rows that overfill the list (sorted ones, many equal values)
+// take a radix selection over the CTA's part of the row instead.
 
 #include <math.h>
 #include <stdint.h>
@@ -42,19 +45,22 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;         // streaming threads of a CTA
 constexpr int kWarps = kThreads / 32;
 constexpr int kVec = 4;              // 16-byte loads per thread and round
-constexpr int kMaxPieces = 32;
-constexpr int kMaxSlots = 4096;      // pieces of cut rows in all
-constexpr int kCap = 1024;           // candidate keys of a stage, the best so far among them
-constexpr int kHits = 512;           // noted threads of a stage
+constexpr int kStages = 4;
+constexpr uint32_t kRoundBytes = kThreads * kVec * 16;
+constexpr int kPerSm = 6;            // CTAs: what the rings leave room for
+constexpr int kMaxCtas = 1024;
+constexpr uint64_t kWaitNs = 2000000000ull;   // any single wait gives up after 2 s
+constexpr int kCap = 256;            // candidate keys of a stage, the best so far among them
 constexpr float kPlain = 16384.0f;   // maxima up to this size take the packed loop
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct LogprobParams {
-    int N, V, top, pieces, rounds;   // rounds per row
+    int N, V, top, rounds, ctas;     // rounds per row
+    long long total;                 // rounds of all entries
     long long ldv, logits_rows;
     const void* logits;
     const int* rows;
@@ -63,10 +69,27 @@ struct LogprobParams {
     float* entropy;
     int* top_ids;
     float* top_logprobs;
-    int* counters;    // [kJoinCounters], zero between calls
-    float4* partial;  // [N][pieces] (m, z, t, -)
-    u64* keys;        // [N][pieces][top]
+    int* counters;    // [ctas], zero between calls: of the entry that ends the CTA's share
+    float4* partial;  // [ctas][2] (m, z, t, -): of the entry that begins the share, and the one that ends it
+    u64* keys;        // [ctas][2][top]
+    int* err;
+
+    __device__ __forceinline__ long long share(int c) const { return total * c / ctas; }
+    // the CTA whose share holds round g
+    __device__ __forceinline__ int owner(long long g) const {
+        int c = (int)(g * ctas / total);
+        while (c + 1 < ctas && share(c + 1) <= g) ++c;
+        while (c > 0 && share(c) > g) --c;
+        return c;
+    }
+    __device__ __forceinline__ long long row_of(int i) const {
+        const long long r = rows ? (long long)__ldg(rows + i) : i;
+        return r >= 0 && r < logits_rows ? r : -1;
+    }
 };
+
+// The streaming warps' own barrier (the copying warp runs ahead of it).
+__device__ __forceinline__ void sync_streams() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
@@ -142,16 +165,17 @@ struct Round<float> {
     static constexpr uint32_t kNegInfWord = 0xff800000u;
 };
 
-// Values v0 .. v0 + 4 * 256 * kPer of the row, this thread's share; past V: -inf.
+// This thread's values of a round in shared memory; pieces past V: -inf.
 template <typename T>
-__device__ __forceinline__ void load_round(uint4 (&q)[kVec], const T* row, int v0, int V) {
+__device__ __forceinline__ void load_round(uint4 (&q)[kVec], const unsigned char* stage, int v0, int V) {
     constexpr int per = Round<T>::kPer;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int v = v0 + (i * kThreads + (int)threadIdx.x) * per;
+    for (int i = 0; i < kVec; ++i) q[i] = reinterpret_cast<const uint4*>(stage)[i * kThreads + (int)threadIdx.x];
+    if (v0 + kThreads * kVec * per > V) {
         const uint32_t ninf = Round<T>::kNegInfWord;
-        q[i] = make_uint4(ninf, ninf, ninf, ninf);
-        if (v < V) q[i] = __ldcs(reinterpret_cast<const uint4*>(row + v));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)   // not copied: whatever the ring held
+            if (v0 + (i * kThreads + (int)threadIdx.x) * per >= V) q[i] = make_uint4(ninf, ninf, ninf, ninf);
     }
 }
 
@@ -200,39 +224,28 @@ __device__ __forceinline__ float round_max(const uint4 (&q)[kVec]) {
     }
 }
 
-// Sort `n` keys of `list` (n <= kCap, every thread calls) by counting; the
-// largest min(n, top) end up first, largest first.  Returns that count.
-__device__ __forceinline__ int keep_best(u64* list, int n, int top) {
-    constexpr int kEach = kCap / kThreads;
-    u64 mine[kEach];
-    int rank[kEach];
-#pragma unroll
-    for (int c = 0; c < kEach; ++c) {
-        const int i = c * kThreads + (int)threadIdx.x;
-        rank[c] = kCap;
-        if (i < n) {
-            mine[c] = list[i];
-            int r = 0;
-            for (int j = 0; j < n; ++j) r += list[j] > mine[c];
-            rank[c] = r;
-        }
+// Sort `n` keys of `from` (n <= kCap, every thread calls, a barrier before) by
+// counting; the largest min(n, top) go to `to`, largest first.  The caller
+// places a barrier before either list is used again.  Returns that count.
+__device__ __forceinline__ int keep_best(const u64* from, u64* to, int n, int top) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const u64 mine = from[i];
+        int r = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) r += from[j] > mine;
+        if (r < top) to[r] = mine;
     }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kEach; ++c)
-        if (rank[c] < top) list[rank[c]] = mine[c];
-    __syncthreads();
     return min(n, top);
 }
 
 struct Shared {
-    u64 list[kCap];
-    int hits[kHits];
-    int hist[256];
-    Sums part[kWarps];
-    uint32_t floor;   // of the first round
+    uint64_t full[kStages], empty[kStages];
+    int abort;
+    u64 lists[2][kCap];   // the one in use, and the other to sort into
+    float part[3][kWarps];
+    uint32_t floors[kWarps];   // of the first round
     uint32_t prefix;
-    int count, n_hits, over, need, last;
+    int count, over, need, last;
 };
 
 template <typename T>
@@ -241,87 +254,65 @@ __device__ __forceinline__ float load_value(const T* row, int v) {
     else return __ldg(row + v);
 }
 
-// Read the noted threads' values again and append the keys above `above`; then
-// keep the best.  Every thread calls; returns how many are kept, sorted.
+// Append the keys above `above` of one round's values of the lanes in `who`, from
+// shared memory.  A whole warp calls.
 template <typename T>
-__device__ __forceinline__ int take_hits(Shared& sh, const T* row, int V, int top, int kept, u64 above) {
+__device__ __forceinline__ void append(Shared& sh, u64* list, const unsigned char* stage, unsigned who, int v0, int V, u64 above) {
     constexpr int per = Round<T>::kPer, values = kVec * per;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int hits = min(sh.n_hits, kHits);
-    if (threadIdx.x == 0) sh.count = kept;
-    __syncthreads();
+    const int lane = threadIdx.x & 31;
     const float low = key_floor(above);
-    constexpr int kAtOnce = 4;
-    for (int h0 = warp * kAtOnce; h0 < hits; h0 += kWarps * kAtOnce) {
-        float x[kAtOnce];
-        int v[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            const int h = h0 + u < hits ? sh.hits[h0 + u] : -1;
-            v[u] = (h / kThreads) * (kThreads * values) + ((lane / per) * kThreads + h % kThreads) * per + lane % per;
-            x[u] = -INFINITY;
-            if (h >= 0 && lane < values && v[u] < V) x[u] = load_value(row, v[u]);
-            else v[u] = -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            if (v[u] < 0 || !(x[u] >= low)) continue;
-            const u64 key = make_key(x[u], v[u]);
-            if (key > above) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kCap) sh.list[at] = key;
+    while (who) {
+        const int thread = (int)(threadIdx.x & ~31u) + __ffs(who) - 1;
+        who &= who - 1;
+        if (lane < values) {
+            const int at = ((lane / per) * kThreads + thread) * per + lane % per;
+            float x;
+            if constexpr (sizeof(T) == 2) x = __uint_as_float((uint32_t)reinterpret_cast<const T*>(stage)[at] << 16);
+            else x = reinterpret_cast<const T*>(stage)[at];
+            if (v0 + at < V && x >= low) {
+                const u64 key = make_key(x, v0 + at);
+                if (key > above) {
+                    const int slot = atomicAdd(&sh.count, 1);
+                    if (slot < kCap) list[slot] = key;
+                }
             }
         }
     }
-    __syncthreads();
-    const int n = sh.count;
-    if (n > kCap || sh.n_hits > kHits) {   // too many to sort: the piece is selected anew at its end
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            sh.over = 1;
-            sh.n_hits = 0;
-        }
-        __syncthreads();
-        return kept;
-    }
-    const int k = keep_best(sh.list, n, top);
-    if (threadIdx.x == 0) sh.n_hits = 0;
-    __syncthreads();
-    return k;
 }
 
-// The best `top` of values [v0, v1) by radix selection, into the list, sorted.
+// The best `top` of values [v0, v1) by radix selection, into `to`, sorted; `list` is
+// used on the way.  Every thread calls; a barrier before and after is the caller's.
 template <typename T>
-__device__ __noinline__ int select_slow(Shared& sh, const T* row, int v0, int v1, int top) {
+__device__ __noinline__ int select_slow(Shared& sh, u64* list, u64* to, const T* row, int v0, int v1, int top) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = v1 - v0;
+    int* const hist = reinterpret_cast<int*>(to);   // 256 counts, until the sort
     if (tid == 0) sh.count = 0;
     if (n <= top) {
-        __syncthreads();
-        for (int v = v0 + tid; v < v1; v += kThreads) sh.list[v - v0] = make_key(load_value(row, v), v);
-        __syncthreads();
-        return keep_best(sh.list, n, top);
+        for (int v = v0 + tid; v < v1; v += kThreads) list[v - v0] = make_key(load_value(row, v), v);
+        sync_streams();
+        return keep_best(list, to, n, top);
     }
     uint32_t prefix = 0;
     int need = top;
     for (int shift = 24; shift >= (sizeof(T) == 2 ? 16 : 0); shift -= 8) {
-        sh.hist[tid] = 0;
-        __syncthreads();
+        for (int k = tid; k < 256; k += kThreads) hist[k] = 0;
+        sync_streams();
         for (int v = v0 + tid; v < v1; v += kThreads) {
             const uint32_t k = ordered(load_value(row, v));
-            if (shift == 24 || ((k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&sh.hist[(k >> shift) & 255], 1);
+            if (shift == 24 || ((k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(k >> shift) & 255], 1);
         }
-        __syncthreads();
+        sync_streams();
         if (tid == 0) {
             int left = need, bin = 255;
-            while (bin > 0 && sh.hist[bin] < left) left -= sh.hist[bin--];
+            while (bin > 0 && hist[bin] < left) left -= hist[bin--];
             sh.prefix = prefix | ((uint32_t)bin << shift);
             sh.need = left;
         }
-        __syncthreads();
+        sync_streams();
         prefix = sh.prefix;
         need = sh.need;
-        __syncthreads();
+        sync_streams();
     }
     // of the values with this prefix (bf16: equal ones) the first `need` tokens
     constexpr uint32_t kBits = sizeof(T) == 2 ? 0xffff0000u : 0xffffffffu;
@@ -332,90 +323,60 @@ __device__ __noinline__ int select_slow(Shared& sh, const T* row, int v0, int v1
         const uint32_t k = ordered(x) & kBits;
         const bool eq = v < v1 && k == prefix;
         const unsigned bal = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) sh.hist[warp] = __popc(bal);
-        __syncthreads();
+        if (lane == 0) hist[warp] = __popc(bal);
+        sync_streams();
         int here = before;
         for (int w = 0; w < kWarps; ++w) {
-            here += w < warp ? sh.hist[w] : 0;
-            before += sh.hist[w];
+            here += w < warp ? hist[w] : 0;
+            before += hist[w];
         }
         if (v < v1 && (k > prefix || (eq && here + __popc(bal & ((1u << lane) - 1u)) < need)))
-            sh.list[atomicAdd(&sh.count, 1)] = make_key(x, v);   // `top` in all
-        __syncthreads();
+            list[atomicAdd(&sh.count, 1)] = make_key(x, v);   // `top` in all
+        sync_streams();
     }
-    return keep_best(sh.list, sh.count, top);
+    return keep_best(list, to, sh.count, top);
 }
 
-// z and t of a round's values above the running m (m is at least their maximum).
+// z and t of a round's values above the running m (m is at least their maximum),
+// as packed pairs.
 template <typename T>
-__device__ __forceinline__ void round_sums(const uint4 (&q)[kVec], float m, u64& z2, u64& t2) {
+__device__ __forceinline__ void round_sums(const uint4 (&q)[kVec], float m, u64& z, u64& t) {
+    if (m == -INFINITY) return;   // nothing yet
     if (fabsf(m) <= kPlain) {
         // values under -2 kPlain are 2^(-20000) = 0 all the same: held there, -inf adds 0 to both sums
-        const u64 c2 = f32x2_splat(kLog2e), n2 = f32x2_splat(-__fmul_rn(m, kLog2e));
-        if constexpr (sizeof(T) == 2) {
+        const u64 c2 = f32x2_splat(kLog2e), cm = f32x2_splat(-__fmul_rn(m, kLog2e));
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        for (int i = 0; i < kVec; ++i) {
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4; k += sizeof(T) == 2 ? 1 : 2) {
+                float lo, hi;
+                if constexpr (sizeof(T) == 2) {
                     const uint32_t x = bf16x2_max(w[k], 0xc700c700u);
-                    asm("{\n\t.reg .b32 l, h;\n\t.reg .b64 y, p;\n\t"
-                        "prmt.b32 l, %2, 0, 0x1044;\n\t"
-                        "and.b32 h, %2, 0xffff0000;\n\t"
-                        "mov.b64 y, {l, h};\n\t"
-                        "fma.rn.f32x2 y, y, %3, %4;\n\t"
-                        "mov.b64 {l, h}, y;\n\t"
-                        "ex2.approx.ftz.f32 l, l;\n\t"
-                        "ex2.approx.ftz.f32 h, h;\n\t"
-                        "mov.b64 p, {l, h};\n\t"
-                        "add.rn.f32x2 %0, %0, p;\n\t"
-                        "fma.rn.f32x2 %1, p, y, %1;\n\t}"
-                        : "+l"(z2), "+l"(t2)
-                        : "r"(x), "l"(c2), "l"(n2));
+                    lo = bf16_lo(x);
+                    hi = bf16_hi(x);
+                } else {
+                    lo = fmaxf(__uint_as_float(w[k]), -2 * kPlain);
+                    hi = fmaxf(__uint_as_float(w[k + 1]), -2 * kPlain);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    const float l = fmaxf(__uint_as_float(w[k]), -2 * kPlain), h = fmaxf(__uint_as_float(w[k + 1]), -2 * kPlain);
-                    asm("{\n\t.reg .b32 l, h;\n\t.reg .b64 y, p;\n\t"
-                        "mov.b64 y, {%2, %3};\n\t"
-                        "fma.rn.f32x2 y, y, %4, %5;\n\t"
-                        "mov.b64 {l, h}, y;\n\t"
-                        "ex2.approx.ftz.f32 l, l;\n\t"
-                        "ex2.approx.ftz.f32 h, h;\n\t"
-                        "mov.b64 p, {l, h};\n\t"
-                        "add.rn.f32x2 %0, %0, p;\n\t"
-                        "fma.rn.f32x2 %1, p, y, %1;\n\t}"
-                        : "+l"(z2), "+l"(t2)
-                        : "f"(l), "f"(h), "l"(c2), "l"(n2));
-                }
+                const u64 y = f32x2_fma(f32x2_pack(lo, hi), c2, cm);
+                const u64 p = f32x2_pack(ex2_approx(f32x2_lo(y)), ex2_approx(f32x2_hi(y)));
+                z = f32x2_add(z, p);
+                t = f32x2_fma(p, y, t);
             }
         }
         return;
     }
-    if (m == -INFINITY) return;   // nothing yet
-    float z = 0.0f, t = 0.0f;
-#pragma unroll 1
-    for (int i = 0; i < kVec * Round<T>::kPer; ++i) {
-        uint4 v = q[0];
 #pragma unroll
-        for (int k = 1; k < kVec; ++k)
-            if (i / Round<T>::kPer == k) v = q[k];
-        const int e = i % Round<T>::kPer;
-        float x = Round<T>::get(v, 0);
+    for (int i = 0; i < kVec; ++i)
 #pragma unroll
-        for (int k = 1; k < Round<T>::kPer; ++k)
-            if (e == k) x = Round<T>::get(v, k);
-        const float y = fmaxf((x - m) * kLog2e, -1e4f), p = ex2_approx(y);
-        z += p;
-        t = fmaf(p, y, t);
-    }
-    z2 = f32x2_add(z2, (u64)__float_as_uint(z));
-    t2 = f32x2_add(t2, (u64)__float_as_uint(t));
+        for (int k = 0; k < Round<T>::kPer; k += 2) {
+            const float ya = fmaxf((Round<T>::get(q[i], k) - m) * kLog2e, -1e4f);
+            const float yb = fmaxf((Round<T>::get(q[i], k + 1) - m) * kLog2e, -1e4f);
+            const u64 p = f32x2_pack(ex2_approx(ya), ex2_approx(yb));
+            z = f32x2_add(z, p);
+            t = f32x2_fma(p, f32x2_pack(ya, yb), t);
+        }
 }
 
 // Results of entry i from its row's sums and its sorted keys.
@@ -440,160 +401,261 @@ __device__ __forceinline__ void write_entry(const LogprobParams& P, int i, const
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const __grid_constant__ LogprobParams P) {
-    __shared__ Shared sh;
+__global__ void __launch_bounds__(kThreads + 32, kPerSm) logprob_kernel(const __grid_constant__ LogprobParams P) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    Shared& sh = *reinterpret_cast<Shared*>(ring + kStages * kRoundBytes);
     constexpr int per = Round<T>::kPer;
     constexpr int kRound = kThreads * kVec * per;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int i = blockIdx.x / P.pieces, piece = blockIdx.x - i * P.pieces;
+    if (tid == 0) {
+        sh.abort = 0;
+        sh.count = sh.over = 0;
+        for (int k = 0; k < kStages; ++k) {
+            mbar_init(smem_addr(&sh.full[k]), 1);
+            mbar_init(smem_addr(&sh.empty[k]), kWarps);
+        }
+        mbar_fence_init();
+    }
+    __syncthreads();
     pdl_wait();
     pdl_release();
-    const long long r = P.rows ? (long long)P.rows[i] : i;
-    const T* row = r >= 0 && r < P.logits_rows ? static_cast<const T*>(P.logits) + r * P.ldv : nullptr;
-    if (!row) {   // the whole row agrees: no piece counts itself
-        if (piece == 0) write_entry<T>(P, i, nullptr, Sums{}, sh.list, 0);
+    const long long g0 = P.share(blockIdx.x), g1 = P.share(blockIdx.x + 1);
+    if (warp == kWarps) {
+        // ---------------------------------------------------------- copies
+        if (lane == 0) {
+            const uint64_t once = l2_policy_evict_first();
+            int i = (int)(g0 / P.rounds), rd = (int)(g0 - (long long)i * P.rounds);
+            long long r = P.row_of(i);
+            for (long long g = g0; g < g1; ++g) {
+                const uint32_t n = (uint32_t)(g - g0), k = n % kStages;
+                if (!mbar_wait_bounded(smem_addr(&sh.empty[k]), (n / kStages & 1) ^ 1, kWaitNs) ||
+                    *(volatile int*)&sh.abort) {
+                    set_error(P.err, DLLM_DEVERR_TIMEOUT);
+                    *(volatile int*)&sh.abort = 1;
+                    break;
+                }
+                const int v0 = rd * kRound;
+                const uint32_t bytes = r < 0 ? 0u : (uint32_t)min(kRoundBytes, (uint32_t)((P.V - v0 + per - 1) / per) * 16u);
+                mbar_arrive_expect_tx(smem_addr(&sh.full[k]), bytes);
+                if (bytes)
+                    bulk_g2s(smem_addr(ring + k * kRoundBytes), static_cast<const T*>(P.logits) + r * P.ldv + v0, bytes,
+                             smem_addr(&sh.full[k]), once);
+                if (++rd == P.rounds && g + 1 < g1) {
+                    rd = 0;
+                    r = P.row_of(++i);
+                }
+            }
+        }
         return;
     }
-    const int first = (int)((long long)P.rounds * piece / P.pieces);
-    const int end = (int)((long long)P.rounds * (piece + 1) / P.pieces);
-    float m = -INFINITY;
-    u64 z2 = 0, t2 = 0;
-    u64 above = 0;        // keys at or under it are not among the best
-    float low = INFINITY; // what a round's maximum must pass to be noted
-    int kept = 0, stage = 1;
-    if (kTop) {
-        if (tid == 0) {
-            sh.n_hits = sh.over = 0;
-            sh.floor = 0xffffffffu;
-        }
-        __syncthreads();
-    }
-    uint4 q[kVec], nx[kVec];
-    load_round<T>(nx, row, first * kRound, P.V);
-    for (int rd = first; rd < end; ++rd) {
-        const int v0 = rd * kRound;
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) q[k] = nx[k];
-        if (rd + 1 < end) load_round<T>(nx, row, v0 + kRound, P.V);
-        if (v0 + kRound > P.V) mask_round<T>(q, v0, P.V);
-        const float bm = round_max<T>(q);
-        if (!(bm <= m)) {
-            const float mn = max_nan(m, bm);
-            const float d = fmaxf(diff2(m, mn), -1e4f), f = ex2_approx(d);
-            const u64 f2 = f32x2_splat(f);
-            t2 = f32x2_mul(f2, f32x2_fma(z2, f32x2_splat(d), t2));
-            z2 = f32x2_mul(z2, f2);
-            m = mn;
-        }
-        round_sums<T>(q, m, z2, t2);
-        if constexpr (kTop) {
-            if (rd == first) {
-                // the first floor, by bits of the order-preserving key from the top (16 of them)
-                const int full = min(max(P.V - v0, 0) / (32 * per), kWarps);   // warps whose lanes all have values
-                const uint32_t key = ordered(bm);
-                uint32_t fl = 0;
-                if (warp < full) {
-                    const int want = (P.top + full - 1) / full;
-#pragma unroll 1
-                    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
-                        const unsigned at = __ballot_sync(0xffffffffu, key >= (fl | bit));
-                        if (__popc(at) >= want) fl |= bit;
-                    }
-                    if (lane == 0) atomicMin(&sh.floor, fl);
-                }
-                __syncthreads();
-                fl = full > 0 ? sh.floor : 0;
-                above = fl ? ((u64)fl << 32) - 1 : 0;   // every key of a value at the floor passes
-                low = key_floor(above + 1);
-                if (bm >= low) {
-                    const int at = atomicAdd(&sh.n_hits, 1);
-                    if (at < kHits) sh.hits[at] = rd * kThreads + tid;
-                }
-            } else if (bm > low || above == 0) {
-                const int at = atomicAdd(&sh.n_hits, 1);
-                if (at < kHits) sh.hits[at] = rd * kThreads + tid;
+    // -------------------------------------------------------------- streams
+    int i = (int)(g0 / P.rounds);
+    for (long long g = g0; g < g1; ++i) {
+        // entry i from round rd0 of its row to `rounds`, as far as the share goes
+        const long long begin = (long long)i * P.rounds;
+        const int rd0 = (int)(g - begin), rd1 = (int)min((long long)P.rounds, g1 - begin);
+        const long long r = P.row_of(i);
+        const T* row = r >= 0 ? static_cast<const T*>(P.logits) + r * P.ldv : nullptr;
+        float m = -INFINITY;
+        u64 z = 0, t = 0;
+        u64 above = 0;        // keys at or under it are not among the best
+        float low = INFINITY; // what a round's maximum must pass to be noted
+        int kept = 0, stage = 1, in_use = 0;
+        for (int rd = rd0; rd < rd1; ++rd, ++g) {
+            const uint32_t n = (uint32_t)(g - g0), k = n % kStages;
+            // once a wait has given up the rest runs through without waiting, every barrier met
+            if (*(volatile int*)&sh.abort == 0 &&
+                !mbar_wait_bounded(smem_addr(&sh.full[k]), n / kStages & 1, kWaitNs)) {
+                set_error(P.err, DLLM_DEVERR_TIMEOUT);
+                *(volatile int*)&sh.abort = 1;
             }
-            if (rd - first + 1 == stage || rd + 1 == end) {
-                stage *= 2;
-                __syncthreads();
-                if (!sh.over) {
-                    kept = take_hits<T>(sh, row, P.V, P.top, kept, above);
-                    if (kept == P.top && !sh.over) {
-                        above = max(above, sh.list[kept - 1]);
+            const int v0 = rd * kRound;
+            uint4 q[kVec];
+            const unsigned char* const in = ring + k * kRoundBytes;
+            load_round<T>(q, in, v0, P.V);
+            if (!row) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.empty[k]));
+                continue;
+            }
+            if (v0 + kRound > P.V) mask_round<T>(q, v0, P.V);
+            const float bm = round_max<T>(q);
+            uint32_t fl = 0;
+            if constexpr (kTop) {
+                if (rd == rd0) {
+                    // the first floor, by bits of the order-preserving key from the top (16 of them)
+                    const int full = min((P.V - v0) / (32 * per), kWarps);   // warps whose lanes all have values
+                    const uint32_t key = ordered(bm);
+                    if (warp < full) {
+                        const int want = (P.top + full - 1) / full;
+#pragma unroll 1
+                        for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+                            const unsigned at = __ballot_sync(0xffffffffu, key >= (fl | bit));
+                            if (__popc(at) >= want) fl |= bit;
+                        }
+                    } else if (full > 0) {
+                        fl = 0xffffffffu;
+                    }
+                    if (lane == 0) sh.floors[warp] = fl;
+                } else {
+                    const unsigned who = __ballot_sync(0xffffffffu, bm > low || above == 0);
+                    if (who) append<T>(sh, sh.lists[in_use], in, who, v0, P.V, above);
+                }
+            }
+            if (!kTop || rd != rd0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.empty[k]));
+            }
+            if (!(bm <= m)) {
+                const float mn = max_nan(m, bm);
+                const float d = fmaxf(diff2(m, mn), -1e4f), f = ex2_approx(d);
+                const u64 f2 = f32x2_splat(f);
+                t = f32x2_mul(f2, f32x2_fma(z, f32x2_splat(d), t));
+                z = f32x2_mul(z, f2);
+                m = mn;
+            }
+            round_sums<T>(q, m, z, t);
+            if constexpr (kTop) {
+                if (rd == rd0) {
+                    sync_streams();
+                    fl = sh.floors[0];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) fl = min(fl, sh.floors[w]);
+                    above = fl ? ((u64)fl << 32) - 1 : 0;   // every key of a value at the floor passes
+                    low = key_floor(above + 1);
+                    append<T>(sh, sh.lists[0], in, __ballot_sync(0xffffffffu, bm >= low), v0, P.V, above);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.empty[k]));
+                }
+                if (rd - rd0 + 1 == stage || rd + 1 == rd1) {
+                    stage *= 4;
+                    sync_streams();
+                    const int n = sh.count;
+                    if (n <= kCap) {
+                        kept = keep_best(sh.lists[in_use], sh.lists[in_use ^ 1], n, P.top);
+                        in_use ^= 1;
+                    }
+                    sync_streams();
+                    // a list that ran over starts again; the part is selected anew at its end
+                    if (n > kCap) kept = 0;
+                    if (tid == 0) {
+                        if (n > kCap) sh.over = 1;
+                        sh.count = kept;
+                    }
+                    if (kept == P.top) {
+                        above = max(above, sh.lists[in_use][kept - 1]);
                         low = key_value(above);
                     }
-                    __syncthreads();   // the list is read before a later stage appends
+                    if (rd + 1 < rd1) sync_streams();   // the count is set before later rounds append
                 }
             }
         }
-    }
-    if constexpr (kTop) {
-        if (sh.over) kept = select_slow<T>(sh, row, first * kRound, min(end * kRound, P.V), P.top);
-    }
-    const float z = __uint_as_float((uint32_t)z2) + __uint_as_float((uint32_t)(z2 >> 32));
-    const float t = __uint_as_float((uint32_t)t2) + __uint_as_float((uint32_t)(t2 >> 32));
-    Sums s{m, z, t};
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        Sums o;
-        o.m = __shfl_xor_sync(0xffffffffu, s.m, off);
-        o.z = __shfl_xor_sync(0xffffffffu, s.z, off);
-        o.t = __shfl_xor_sync(0xffffffffu, s.t, off);
-        s = (lane & off) ? join(o, s) : join(s, o);
-    }
-    if (lane == 0) sh.part[warp] = s;
-    __syncthreads();
-    s = sh.part[0];
-    for (int w = 1; w < kWarps; ++w) s = join(s, sh.part[w]);
-    if (P.pieces == 1) {
-        write_entry<T>(P, i, row, s, sh.list, kept);
-        return;
-    }
-    const long long slot = (long long)i * P.pieces;
-    if (tid == 0) P.partial[slot + piece] = make_float4(s.m, s.z, s.t, 0.0f);
-    if constexpr (kTop) {
-        for (int k = tid; k < P.top; k += kThreads)
-            P.keys[(slot + piece) * P.top + k] = k < kept ? sh.list[k] : 0ull;
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) sh.last = atom_add_acqrel_gpu(P.counters + i, 1) == P.pieces - 1;
-    __syncthreads();
-    if (!sh.last) return;
-    __threadfence();
-    if (tid == 0) P.counters[i] = 0;
-    const float4 p0 = __ldcg(P.partial + slot);
-    s = Sums{p0.x, p0.y, p0.z};
-    for (int k = 1; k < P.pieces; ++k) {
-        const float4 p = __ldcg(P.partial + slot + k);
-        s = join(s, Sums{p.x, p.y, p.z});
-    }
-    int n = 0;
-    if constexpr (kTop) {
-        if (tid == 0) sh.count = 0;
-        __syncthreads();
-        for (int k = tid; k < P.pieces * P.top; k += kThreads) {
-            const u64 key = __ldcg(P.keys + slot * P.top + k);
-            if (key) sh.list[atomicAdd(&sh.count, 1)] = key;   // pieces * top <= kCap
+        if (kTop && row) {
+            sync_streams();
+            if (sh.over) {
+                kept = select_slow<T>(sh, sh.lists[in_use], sh.lists[in_use ^ 1], row, rd0 * kRound, min(rd1 * kRound, P.V), P.top);
+                in_use ^= 1;
+                sync_streams();
+            }
         }
-        __syncthreads();
-        n = keep_best(sh.list, sh.count, P.top);
+        // the CTA's sums: the maximum first, then every thread moves its sums to it once
+        Sums s;
+        s.m = m;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) s.m = max_nan(s.m, __shfl_xor_sync(0xffffffffu, s.m, off));
+        if (lane == 0) sh.part[0][warp] = s.m;
+        sync_streams();
+        if (kTop && tid == 0) sh.count = sh.over = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s.m = max_nan(s.m, sh.part[0][w]);
+        {
+            const float d = fmaxf(diff2(m, s.m), -1e4f), f = ex2_approx(d);   // m -inf: z is 0
+            const float zz = f32x2_lo(z) + f32x2_hi(z);
+            s.z = f * zz;
+            s.t = f * (f32x2_lo(t) + f32x2_hi(t) + zz * d);
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            s.z += __shfl_xor_sync(0xffffffffu, s.z, off);
+            s.t += __shfl_xor_sync(0xffffffffu, s.t, off);
+        }
+        if (lane == 0) {
+            sh.part[1][warp] = s.z;
+            sh.part[2][warp] = s.t;
+        }
+        sync_streams();
+        s.z = s.t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s.z += sh.part[1][w];
+            s.t += sh.part[2][w];
+        }
+        if (rd0 == 0 && rd1 == P.rounds) {
+            write_entry<T>(P, i, row, s, sh.lists[in_use], kept);
+        } else if (!row) {
+            if (rd0 == 0) write_entry<T>(P, i, nullptr, s, nullptr, 0);   // all parts agree: none counts itself
+        } else {
+            // the parts of an entry: the last of CTA c0's share, then the first of c0 + 1 .. c1
+            const int c0 = P.owner(begin), c1 = P.owner(begin + P.rounds - 1);
+            const int mine = blockIdx.x == c0 && begin > g0 ? 1 : 0;
+            const long long slot = (long long)blockIdx.x * 2 + mine;
+            if (tid == 0) __stcg(P.partial + slot, make_float4(s.m, s.z, s.t, 0.0f));
+            if constexpr (kTop) {
+                for (int k = tid; k < P.top; k += kThreads) __stcg(P.keys + slot * P.top + k, k < kept ? sh.lists[in_use][k] : 0ull);
+            }
+            __threadfence();
+            sync_streams();
+            if (tid == 0) sh.last = atom_add_acqrel_gpu(P.counters + c0, 1) == c1 - c0;
+            sync_streams();
+            if (sh.last) {
+                __threadfence();
+                if (tid == 0) P.counters[c0] = 0;
+                auto slot_of = [&](int c) { return (long long)c * 2 + (c == c0 && begin > P.share(c0) ? 1 : 0); };
+                s = Sums{-INFINITY, 0.0f, 0.0f};
+                if (tid == 0) sh.count = 0;
+                sync_streams();
+                for (int c = c0; c <= c1; ++c) {
+                    const float4 p = __ldcg(P.partial + slot_of(c));
+                    s = join(s, Sums{p.x, p.y, p.z});
+                }
+                int n = 0;
+                if constexpr (kTop) {
+                    // batches that fit the list beside the best so far
+                    const int batch = (kCap - P.top) / P.top;
+                    for (int c = c0; c <= c1; c += batch) {
+                        u64* const list = sh.lists[in_use];
+                        const int here = min(batch, c1 - c + 1);
+                        for (int k = tid; k < here * P.top; k += kThreads) {
+                            const u64 key = __ldcg(P.keys + slot_of(c + k / P.top) * P.top + k % P.top);
+                            if (key) list[n + atomicAdd(&sh.count, 1)] = key;
+                        }
+                        sync_streams();
+                        const int all = n + sh.count;
+                        n = keep_best(list, sh.lists[in_use ^ 1], all, P.top);
+                        in_use ^= 1;
+                        sync_streams();
+                        if (tid == 0) sh.count = 0;
+                        sync_streams();
+                    }
+                }
+                write_entry<T>(P, i, row, s, sh.lists[in_use], n);
+            }
+        }
+        sync_streams();   // the list and the parts are free
     }
-    write_entry<T>(P, i, row, s, sh.list, n);
 }
 
 inline int round_values(int dtype) { return kThreads * kVec * (dtype == DLLM_DTYPE_F32 ? 4 : 8); }
 
-// Pieces per row.  One CTA per row leaves SMs idle until there are a few rows
-// per resident CTA (3 per SM); below that rows are cut, at most to single
-// rounds, so that about 4 waves of CTAs are there to balance.
-inline int pick_pieces(int N, int V, int top, int dtype, int sms) {
-    const int rounds = (V + round_values(dtype) - 1) / round_values(dtype);
-    const long long want = ((long long)sms * 12 + N - 1) / std::max(N, 1);
-    if (N > kJoinCounters) return 1;
-    long long p = std::min<long long>({(long long)rounds, want, (long long)kMaxPieces, (long long)kMaxSlots / N});
-    if (top > 0) p = std::min<long long>(p, kCap / top);
-    return (int)std::max<long long>(p, 1);
+constexpr size_t kSmem = kStages * kRoundBytes + sizeof(Shared);
+static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "the CTAs share an SM's shared memory");
+
+template <typename T, bool kTop>
+int launch(const LogprobParams& P, cudaStream_t s) {
+    auto kernel = logprob_kernel<T, kTop>;
+    DLLM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+    DLLM_CUDA_TRY(launch_dependent(kernel, dim3(P.ctas), dim3(kThreads + 32), kSmem, s, P));
+    return DLLM_OK;
 }
 
 }  // namespace
@@ -603,7 +665,7 @@ using namespace dllm;
 
 extern "C" size_t dllm_logprobs_workspace_size(int32_t N, int32_t V, int32_t top) {
     if (N < 0 || V < 1 || top < 0 || top > DLLM_MAX_TOP) return 0;
-    return size_t(kJoinCounters) * 4 + size_t(kMaxSlots) * (sizeof(float4) + size_t(top) * 8);
+    return size_t(kJoinCounters) * 4 + size_t(kMaxCtas) * 2 * (sizeof(float4) + size_t(top) * 8);
 }
 
 extern "C" int dllm_logprobs(const dllm_logprobs_args* a, void* stream) {
@@ -625,8 +687,9 @@ extern "C" int dllm_logprobs(const dllm_logprobs_args* a, void* stream) {
     P.N = a->N;
     P.V = a->V;
     P.top = a->top;
-    P.pieces = pick_pieces(a->N, a->V, a->top, a->dtype, sms);
     P.rounds = (a->V + round_values(a->dtype) - 1) / round_values(a->dtype);
+    P.total = (long long)a->N * P.rounds;
+    P.ctas = (int)std::min<long long>(P.total, std::min(sms * kPerSm, kMaxCtas));
     P.ldv = a->ldv;
     P.logits_rows = a->logits_rows;
     P.logits = a->logits;
@@ -640,12 +703,11 @@ extern "C" int dllm_logprobs(const dllm_logprobs_args* a, void* stream) {
     P.counters = reinterpret_cast<int*>(ws);
     ws += size_t(kJoinCounters) * 4;
     P.partial = reinterpret_cast<float4*>(ws);
-    ws += size_t(kMaxSlots) * sizeof(float4);
+    ws += size_t(kMaxCtas) * 2 * sizeof(float4);
     P.keys = reinterpret_cast<u64*>(ws);
-    const long long grid = (long long)a->N * P.pieces;
-    if (grid > 0x7fffffffll) return DLLM_ERR_UNSUPPORTED;
-    auto kernel = a->dtype == DLLM_DTYPE_F32 ? (a->top ? logprob_kernel<float, true> : logprob_kernel<float, false>)
-                                             : (a->top ? logprob_kernel<uint16_t, true> : logprob_kernel<uint16_t, false>);
-    DLLM_CUDA_TRY(launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), 0, as_stream(stream), P));
-    return DLLM_OK;
+    P.err = error_word_ptr();
+    if (!P.err) return DLLM_ERR_CUDA;
+    cudaStream_t s = as_stream(stream);
+    if (a->dtype == DLLM_DTYPE_F32) return a->top ? launch<float, true>(P, s) : launch<float, false>(P, s);
+    return a->top ? launch<uint16_t, true>(P, s) : launch<uint16_t, false>(P, s);
 }
