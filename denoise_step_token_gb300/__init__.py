@@ -696,18 +696,56 @@ def refill(A0, new_rid, new_p, new_K, new_thr, rid, p, b, K, thr, input_ids, con
 # operators around the step: token reports and the 4-bit cache
 # ---------------------------------------------------------------------------
 _stream_ws = {}
+_size_cache = {}
 
 
-def _workspace(device, nbytes):
-    """A zero-initialised workspace of this device's current stream, grown on
-    demand (calls on different streams may overlap: each has its own)."""
-    torch = _torch()
-    stream = torch.cuda.current_stream(device).cuda_stream
-    cur = _stream_ws.get((device.index, stream))
+def _check_tensors(torch, dev, *tensors):
+    """Every given tensor contiguous on CUDA device ``dev``."""
+    if dev.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
+    for t in tensors:
+        if t is not None:
+            if t.device != dev:
+                raise ValueError("tensors live on different devices")
+            if not t.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+
+
+def _raw_stream(torch, dev):
+    """The handle of the device's current stream, and the call made on the
+    device it belongs to."""
+    if torch.cuda.current_device() != dev.index:
+        raise ValueError("the tensors' device is not the current device")
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _workspace(torch, dev, stream, nbytes):
+    """A zero-initialised workspace of one stream, grown on demand (calls on
+    different streams may overlap: each has its own)."""
+    cur = _stream_ws.get((dev.index, stream))
     if cur is None or cur.numel() < nbytes:
-        cur = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _stream_ws[(device.index, stream)] = cur
+        cur = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+        _stream_ws[(dev.index, stream)] = cur
     return cur
+
+
+def _logprobs_size(lib, N, V, top):
+    n = _size_cache.get((N, V, top))
+    if n is None:
+        n = _size_cache[(N, V, top)] = int(lib.dllm_logprobs_workspace_size(N, V, top))
+        if len(_size_cache) > 4096:
+            _size_cache.clear()
+    return n
+
+
+def _attend_size(lib, cache, L, q_heads):
+    key = (cache.B, cache.heads, cache.page_size, cache.head_dim, L, q_heads)
+    n = _size_cache.get(key)
+    if n is None:
+        n = _size_cache[key] = int(lib.dllm_kv4_attend_workspace_size(ctypes.byref(cache), L, q_heads))
+        if len(_size_cache) > 4096:
+            _size_cache.clear()
+    return n
 
 
 def token_logprobs(logits, tokens, *, V=None, top=0, rows=None, workspace=None):
@@ -724,31 +762,36 @@ def token_logprobs(logits, tokens, *, V=None, top=0, rows=None, workspace=None):
     Returns a dict: logprob and entropy (float32 [N]) and, with top, top_ids
     (int32 [N, top]) and top_logprobs (float32 [N, top]), largest first."""
     torch = _torch()
-    dev = _require_cuda(logits, tokens, rows)
-    if logits.dtype not in (torch.bfloat16, torch.float32):
+    dev = logits.device
+    _check_tensors(torch, dev, logits, tokens, rows)
+    bf16 = logits.dtype == torch.bfloat16
+    if not bf16 and logits.dtype != torch.float32:
         raise TypeError("logits must be bf16 or float32")
-    if tokens.dtype != torch.int32 or (rows is not None and rows.dtype != torch.int32):
+    int32 = torch.int32
+    if tokens.dtype != int32 or (rows is not None and rows.dtype != int32):
         raise TypeError("tokens and rows int32 expected")
     N = tokens.numel()
     ldv = logits.shape[-1]
     n_rows = logits.numel() // ldv if ldv else 0
-    if (rows.numel() if rows is not None else N) != N or (rows is None and n_rows < N):
+    if n_rows < N if rows is None else rows.numel() != N:
         raise ValueError("one row per token")
-    out = {"logprob": torch.empty(N, dtype=torch.float32, device=dev),
-           "entropy": torch.empty(N, dtype=torch.float32, device=dev)}
+    float32, empty = torch.float32, torch.empty
+    out = {"logprob": empty(N, dtype=float32, device=dev), "entropy": empty(N, dtype=float32, device=dev)}
+    ids_p = top_p = None
     if top > 0:
-        out["top_ids"] = torch.empty((N, top), dtype=torch.int32, device=dev)
-        out["top_logprobs"] = torch.empty((N, top), dtype=torch.float32, device=dev)
-    lib = load()
+        out["top_ids"] = ids = empty((N, top), dtype=int32, device=dev)
+        out["top_logprobs"] = lps = empty((N, top), dtype=float32, device=dev)
+        ids_p, top_p = ids.data_ptr(), lps.data_ptr()
+    lib = _lib or load()
     V = ldv if V is None else V
-    ws = workspace
-    if ws is None:
-        ws = _workspace(dev, lib.dllm_logprobs_workspace_size(N, V, top))
-    a = LogprobsArgs(N, V, top, 0 if logits.dtype == torch.bfloat16 else 1, ldv, n_rows, logits.data_ptr(),
+    stream = _raw_stream(torch, dev)
+    ws = _workspace(torch, dev, stream, _logprobs_size(lib, N, V, top)) if workspace is None else workspace
+    a = LogprobsArgs(N, V, top, 0 if bf16 else 1, ldv, n_rows, logits.data_ptr(),
                      None if rows is None else rows.data_ptr(), tokens.data_ptr(), out["logprob"].data_ptr(),
-                     out["entropy"].data_ptr(), out["top_ids"].data_ptr() if top > 0 else None,
-                     out["top_logprobs"].data_ptr() if top > 0 else None, ws.data_ptr(), ws.numel())
-    _check("dllm_logprobs", lib.dllm_logprobs(ctypes.byref(a), _stream(dev)))
+                     out["entropy"].data_ptr(), ids_p, top_p, ws.data_ptr(), ws.numel())
+    rc = lib.dllm_logprobs(ctypes.byref(a), stream)
+    if rc:
+        _check("dllm_logprobs", rc)
     return out
 
 
@@ -763,23 +806,28 @@ def kv4_pages(n_pages, heads, page_size, head_dim, device):
             torch.zeros((n_pages, heads, page_size), dtype=torch.float32, device=device))
 
 
-def _kv4_cache(pages, table, page_size, head_dim):
-    torch = _torch()
+def _kv4_cache(torch, pages, table, page_size, head_dim):
     if pages.dtype != torch.uint8 or pages.dim() != 3:
         raise TypeError("pages must be uint8 [n_pages, heads, bytes]")
     if table.dtype != torch.int32 or table.dim() != 2:
         raise TypeError("the page table must be int32 [B, max_pages]")
     n_pages, heads, nbytes = pages.shape
+    B, max_pages = table.shape
     if nbytes != page_size * (head_dim + head_dim // 8):
         raise ValueError("pages do not hold whole pages of this head_dim")
-    return Kv4Cache(n_pages, heads, page_size, head_dim, table.shape[0], table.shape[1], pages.data_ptr(),
-                    table.data_ptr())
+    return Kv4Cache(n_pages, heads, page_size, head_dim, B, max_pages, pages.data_ptr(), table.data_ptr())
 
 
-def _int32_rows(name, t, n):
-    torch = _torch()
-    if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+def _int32_rows(torch, name, t, n):
+    """The address of an int32 [n] tensor, None for None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n:
         raise TypeError(f"{name} must be int32 [{n}]")
+    return t.data_ptr()
+
+
+_i64x3 = _i64 * 3
 
 
 def kv4_write(k, v, pages, table, pos, *, first=None, count=None, k_out=None, v_out=None):
@@ -795,26 +843,36 @@ def kv4_write(k, v, pages, table, pos, *, first=None, count=None, k_out=None, v_
     k_out, v_out: bf16 [B, W, heads, D] or None: what the cache now holds, in
               the written columns"""
     torch = _torch()
-    dev = _require_cuda(pages, table, pos, first, count, k_out, v_out)
+    dev = pages.device
+    _check_tensors(torch, dev, pages, table, pos, first, count, k_out, v_out)
     if k.device != dev or v.device != dev:
         raise ValueError("tensors live on different devices")
-    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 4 or k.shape != v.shape:
+    bf16, shape = torch.bfloat16, k.shape
+    if k.dtype != bf16 or v.dtype != bf16 or len(shape) != 4 or shape != v.shape:
         raise TypeError("k and v must be bf16 [B, W, heads, D]")
-    B, W, heads, D = k.shape
-    if k.stride(3) != 1 or v.stride(3) != 1:
+    B, W, heads, D = shape
+    kb, kt, kh, kc = k.stride()
+    vb, vt, vh, vc = v.stride()
+    if kc != 1 or vc != 1:
         raise ValueError("the channels of k and v must be contiguous")
-    if table.shape[0] != B or pages.shape[1] != heads:
+    cache = _kv4_cache(torch, pages, table, pages.shape[2] // (D + D // 8), D)
+    if cache.B != B or cache.heads != heads:
         raise ValueError("k, v, pages and table disagree about requests or heads")
-    for name, t in (("pos", pos), ("first", first), ("count", count)):
-        _int32_rows(name, t, B)
-    for t in (k_out, v_out):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != k.shape):
-            raise TypeError("k_out and v_out must be bf16 like k")
-    a = Kv4WriteArgs(_kv4_cache(pages, table, pages.shape[2] // (D + D // 8), D), W, 0, k.data_ptr(), v.data_ptr(),
-                     (_i64 * 3)(*k.stride()[:3]), (_i64 * 3)(*v.stride()[:3]), pos.data_ptr(),
-                     None if first is None else first.data_ptr(), None if count is None else count.data_ptr(),
-                     None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr())
-    _check("dllm_kv4_write", load().dllm_kv4_write(ctypes.byref(a), _stream(dev)))
+    ko = vo = None
+    if k_out is not None:
+        if k_out.dtype != bf16 or k_out.shape != shape:
+            raise TypeError("k_out must be bf16 like k")
+        ko = k_out.data_ptr()
+    if v_out is not None:
+        if v_out.dtype != bf16 or v_out.shape != shape:
+            raise TypeError("v_out must be bf16 like v")
+        vo = v_out.data_ptr()
+    a = Kv4WriteArgs(cache, W, 0, k.data_ptr(), v.data_ptr(), _i64x3(kb, kt, kh), _i64x3(vb, vt, vh),
+                     _int32_rows(torch, "pos", pos, B), _int32_rows(torch, "first", first, B),
+                     _int32_rows(torch, "count", count, B), ko, vo)
+    rc = (_lib or load()).dllm_kv4_write(ctypes.byref(a), _raw_stream(torch, dev))
+    if rc:
+        _check("dllm_kv4_write", rc)
 
 
 def kv4_attend(q, pages, table, lens, *, scale=None, prior=None, weights=None, workspace=None):
@@ -830,33 +888,38 @@ def kv4_attend(q, pages, table, lens, *, scale=None, prior=None, weights=None, w
     Returns a dict: out (bf16 like q, contiguous), lse (float32 [B, L,
     q_heads]) and, where given, weights."""
     torch = _torch()
-    dev = _require_cuda(pages, table, lens, prior, weights)
+    dev = pages.device
+    _check_tensors(torch, dev, pages, table, lens, prior, weights)
     if q.device != dev:
         raise ValueError("tensors live on different devices")
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.stride(3) != 1:
-        raise TypeError("q must be bf16 [B, L, q_heads, D] with contiguous channels")
-    B, L, q_heads, D = q.shape
+    shape = q.shape
+    if q.dtype != torch.bfloat16 or len(shape) != 4:
+        raise TypeError("q must be bf16 [B, L, q_heads, D]")
+    B, L, q_heads, D = shape
+    qb, ql, qh, qc = q.stride()
+    if qc != 1:
+        raise ValueError("the channels of q must be contiguous")
     page_size = pages.shape[2] // (D + D // 8)
-    if table.shape[0] != B:
+    cache = _kv4_cache(torch, pages, table, page_size, D)
+    if cache.B != B:
         raise ValueError("q and table disagree about the requests")
-    _int32_rows("lens", lens, B)
     for t in (prior, weights):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (pages.shape[0], pages.shape[1], page_size)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (cache.n_pages, cache.heads, page_size)):
             raise TypeError("prior and weights must be float32 [n_pages, heads, page_size]")
-    cache = _kv4_cache(pages, table, page_size, D)
-    out = {"out": torch.empty((B, L, q_heads, D), dtype=torch.bfloat16, device=dev),
+    out = {"out": torch.empty(shape, dtype=torch.bfloat16, device=dev),
            "lse": torch.empty((B, L, q_heads), dtype=torch.float32, device=dev)}
     if weights is not None:
         out["weights"] = weights
-    lib = load()
-    ws = workspace
-    if ws is None:
-        ws = _workspace(dev, lib.dllm_kv4_attend_workspace_size(ctypes.byref(cache), L, q_heads))
-    a = Kv4AttendArgs(cache, L, q_heads, D ** -0.5 if scale is None else scale, 0, q.data_ptr(),
-                      (_i64 * 3)(*q.stride()[:3]), lens.data_ptr(), out["out"].data_ptr(), out["lse"].data_ptr(),
+    lib = _lib or load()
+    stream = _raw_stream(torch, dev)
+    ws = _workspace(torch, dev, stream, _attend_size(lib, cache, L, q_heads)) if workspace is None else workspace
+    a = Kv4AttendArgs(cache, L, q_heads, D ** -0.5 if scale is None else scale, 0, q.data_ptr(), _i64x3(qb, ql, qh),
+                      _int32_rows(torch, "lens", lens, B), out["out"].data_ptr(), out["lse"].data_ptr(),
                       None if prior is None else prior.data_ptr(), None if weights is None else weights.data_ptr(),
                       ws.data_ptr(), ws.numel())
-    _check("dllm_kv4_attend", lib.dllm_kv4_attend(ctypes.byref(a), _stream(dev)))
+    rc = lib.dllm_kv4_attend(ctypes.byref(a), stream)
+    if rc:
+        _check("dllm_kv4_attend", rc)
     return out
 
 
@@ -869,19 +932,21 @@ def kv4_evict(pages, weights, table, lens, keep, dst_table, *, recent=0):
     Returns a dict: lens (int32 [B], the new lengths) and src (int32 [B, heads,
     dst_max_pages * page_size], where each token came from; -1 past the end)."""
     torch = _torch()
-    dev = _require_cuda(pages, weights, table, lens, keep, dst_table)
+    dev = pages.device
+    _check_tensors(torch, dev, pages, weights, table, lens, keep, dst_table)
     if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[:2] != pages.shape[:2]:
         raise TypeError("weights must be float32 [n_pages, heads, page_size]")
-    B, page_size = table.shape[0], weights.shape[2]
-    D = pages.shape[2] // page_size * 8 // 9
+    page_size = weights.shape[2]
+    cache = _kv4_cache(torch, pages, table, page_size, pages.shape[2] // page_size * 8 // 9)
+    B, heads = cache.B, cache.heads
     if dst_table.dtype != torch.int32 or dst_table.dim() != 2 or dst_table.shape[0] != B:
         raise TypeError("dst_table must be int32 [B, dst_max_pages]")
-    _int32_rows("lens", lens, B)
-    _int32_rows("keep", keep, B)
-    heads, most = pages.shape[1], dst_table.shape[1]
-    out = {"lens": torch.empty(B, dtype=torch.int32, device=dev),
-           "src": torch.empty((B, heads, most * page_size), dtype=torch.int32, device=dev)}
-    a = Kv4EvictArgs(_kv4_cache(pages, table, page_size, D), recent, most, lens.data_ptr(), keep.data_ptr(),
-                     weights.data_ptr(), dst_table.data_ptr(), out["lens"].data_ptr(), out["src"].data_ptr())
-    _check("dllm_kv4_evict", load().dllm_kv4_evict(ctypes.byref(a), _stream(dev)))
-    return out
+    most = dst_table.shape[1]
+    new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    src = torch.empty((B, heads, most * page_size), dtype=torch.int32, device=dev)
+    a = Kv4EvictArgs(cache, recent, most, _int32_rows(torch, "lens", lens, B), _int32_rows(torch, "keep", keep, B),
+                     weights.data_ptr(), dst_table.data_ptr(), new_lens.data_ptr(), src.data_ptr())
+    rc = (_lib or load()).dllm_kv4_evict(ctypes.byref(a), _raw_stream(torch, dev))
+    if rc:
+        _check("dllm_kv4_evict", rc)
+    return {"lens": new_lens, "src": src}

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "dllm.h"
@@ -42,6 +43,22 @@ int sm_count();
 // lands on another's counters, whatever their shapes: one workspace may serve
 // both.
 constexpr int kJoinCounters = 2048;
+
+// Let `kernel` use `bytes` of dynamic shared memory, once per device (`done`: a
+// static of the caller's, one per kernel; a race repeats the call).
+struct SmemOnce {
+    std::atomic<uint64_t> devices{0};
+};
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, size_t bytes, SmemOnce& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.devices.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done.devices.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 

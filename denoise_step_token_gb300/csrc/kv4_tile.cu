@@ -971,7 +971,8 @@ template <int D, bool kRows2>
 int launch_tile(const AttendParams& P, cudaStream_t s) {
     using T = TileShape<D, kRows2>;
     auto kernel = kv4_tile_kernel<D, kRows2>;
-    DLLM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem));
+    static SmemOnce done;
+    DLLM_CUDA_TRY(allow_smem(kernel, T::kSmem, done));
     DLLM_CUDA_TRY(launch_dependent(kernel, dim3(P.ctas), dim3(kTileThreads), T::kSmem, s, P));
     return DLLM_OK;
 }
@@ -993,7 +994,8 @@ int launch_attend_tiles(const AttendParams& P, int D, cudaStream_t s) {
 template <int D>
 int launch_weights(const AttendParams& P, cudaStream_t s) {
     auto kernel = kv4_weight_tile_kernel<D>;
-    DLLM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WeightShape<D>::kSmem));
+    static SmemOnce done;
+    DLLM_CUDA_TRY(allow_smem(kernel, WeightShape<D>::kSmem, done));
     DLLM_CUDA_TRY(launch_dependent(kernel, dim3(P.ctas), dim3(kTileThreads), WeightShape<D>::kSmem, s, P));
     return DLLM_OK;
 }

@@ -653,7 +653,8 @@ static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "the CTAs share an SM's sha
 template <typename T, bool kTop>
 int launch(const LogprobParams& P, cudaStream_t s) {
     auto kernel = logprob_kernel<T, kTop>;
-    DLLM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+    static SmemOnce done;
+    DLLM_CUDA_TRY(allow_smem(kernel, kSmem, done));
     DLLM_CUDA_TRY(launch_dependent(kernel, dim3(P.ctas), dim3(kThreads + 32), kSmem, s, P));
     return DLLM_OK;
 }

@@ -816,7 +816,8 @@ size_t dllm_kv4_page_bytes(int32_t page_size, int32_t head_dim);
  *   - strides in elements, multiples of 8, channels contiguous, base 16-byte
  *     aligned; k_out / v_out are contiguous [B][W][heads][D] (columns not
  *     written are left as they were).
- * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+ * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED (also W *
+ * heads * D above 2^32), DLLM_ERR_CUDA. */
 typedef struct dllm_kv4_write_args {
     dllm_kv4_cache cache;
     int32_t W;                  /* columns (>= 0) */
