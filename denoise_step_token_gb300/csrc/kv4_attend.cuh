@@ -20,7 +20,8 @@ struct alignas(16) TileItem {
     int b, head, rb;
     int t0, t1;    // tiles; both 0: a request without tokens
     int slot;      // where its partial result goes, -1: it is whole
-    int pad[2];
+    int n;         // the request's tokens
+    int pad;
 };
 // The partial results to join.
 struct alignas(16) TileSplit {
