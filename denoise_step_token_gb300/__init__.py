@@ -719,14 +719,30 @@ def _raw_stream(torch, dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _workspace(torch, dev, stream, nbytes):
+class _StreamWorkspace:
     """A zero-initialised workspace of one stream, grown on demand (calls on
-    different streams may overlap: each has its own)."""
-    cur = _stream_ws.get((dev.index, stream))
-    if cur is None or cur.numel() < nbytes:
-        cur = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
-        _stream_ws[(dev.index, stream)] = cur
-    return cur
+    different streams may overlap: each has its own).  ``lock`` is held from a
+    call's first launch to its last: threads may call on the same stream, and
+    launches of another call must not come between."""
+
+    def __init__(self):
+        self.lock = threading.Lock()
+        self.buf = None
+
+
+def _call(torch, fn, args, dev, stream, nbytes, workspace):
+    """fn(args, stream) with the caller's workspace, or the stream's own."""
+    if workspace is not None:
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        return fn(ctypes.byref(args), stream)
+    key = (dev.index, stream)
+    own = _stream_ws.get(key) or _stream_ws.setdefault(key, _StreamWorkspace())
+    with own.lock:
+        ws = own.buf
+        if ws is None or ws.numel() < nbytes:
+            ws = own.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+        args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
+        return fn(ctypes.byref(args), stream)
 
 
 def _logprobs_size(lib, N, V, top):
@@ -785,11 +801,10 @@ def token_logprobs(logits, tokens, *, V=None, top=0, rows=None, workspace=None):
     lib = _lib or load()
     V = ldv if V is None else V
     stream = _raw_stream(torch, dev)
-    ws = _workspace(torch, dev, stream, _logprobs_size(lib, N, V, top)) if workspace is None else workspace
     a = LogprobsArgs(N, V, top, 0 if bf16 else 1, ldv, n_rows, logits.data_ptr(),
                      None if rows is None else rows.data_ptr(), tokens.data_ptr(), out["logprob"].data_ptr(),
-                     out["entropy"].data_ptr(), ids_p, top_p, ws.data_ptr(), ws.numel())
-    rc = lib.dllm_logprobs(ctypes.byref(a), stream)
+                     out["entropy"].data_ptr(), ids_p, top_p, None, 0)
+    rc = _call(torch, lib.dllm_logprobs, a, dev, stream, _logprobs_size(lib, N, V, top), workspace)
     if rc:
         _check("dllm_logprobs", rc)
     return out
@@ -912,12 +927,11 @@ def kv4_attend(q, pages, table, lens, *, scale=None, prior=None, weights=None, w
         out["weights"] = weights
     lib = _lib or load()
     stream = _raw_stream(torch, dev)
-    ws = _workspace(torch, dev, stream, _attend_size(lib, cache, L, q_heads)) if workspace is None else workspace
     a = Kv4AttendArgs(cache, L, q_heads, D ** -0.5 if scale is None else scale, 0, q.data_ptr(), _i64x3(qb, ql, qh),
                       _int32_rows(torch, "lens", lens, B), out["out"].data_ptr(), out["lse"].data_ptr(),
                       None if prior is None else prior.data_ptr(), None if weights is None else weights.data_ptr(),
-                      ws.data_ptr(), ws.numel())
-    rc = lib.dllm_kv4_attend(ctypes.byref(a), stream)
+                      None, 0)
+    rc = _call(torch, lib.dllm_kv4_attend, a, dev, stream, _attend_size(lib, cache, L, q_heads), workspace)
     if rc:
         _check("dllm_kv4_attend", rc)
     return out

@@ -759,7 +759,9 @@ typedef struct dllm_logprobs_args {
     float* top_logprobs;        /* device [N][top] out (NULL when top is 0) */
     void* workspace;            /* device, >= dllm_logprobs_workspace_size() bytes, 256-byte aligned,
                                    zero-filled before first use; every completed call leaves it ready
-                                   for the next; calls sharing it must be ordered on one stream */
+                                   for the next; calls sharing it must be ordered on one stream, every
+                                   launch of one before the first of the next: threads that share it
+                                   take turns, a whole call each */
     size_t workspace_bytes;
 } dllm_logprobs_args;
 

@@ -1,0 +1,75 @@
+"""The default workspace of token_logprobs and kv4_attend, on the CPU.
+
+The library is replaced by one that records the workspace each call is given,
+and the checks that ask for a CUDA device are taken out: what is tested is which
+memory a call gets, and who else may be using it."""
+import threading
+import time
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import denoise_step_token_gb300 as pkg
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """Records (entry, workspace) and (exit, workspace) of every call, in order."""
+    log = []
+    state = SimpleNamespace(log=log, hold=0.0, seen=None)
+
+    def call(ref, stream):
+        args = ref._obj
+        log.append(("in", args.workspace))
+        if state.seen is not None:
+            state.seen(args)
+        time.sleep(state.hold)
+        log.append(("out", args.workspace))
+        return 0
+
+    lib = SimpleNamespace(dllm_logprobs=call, dllm_kv4_attend=call, dllm_logprobs_workspace_size=lambda *a: 5000,
+                          dllm_kv4_attend_workspace_size=lambda *a: 9000)
+    monkeypatch.setattr(pkg, "_lib", lib)
+    monkeypatch.setattr(pkg, "_check_tensors", lambda *a: None)
+    monkeypatch.setattr(pkg, "_raw_stream", lambda *a: 7)
+    monkeypatch.setattr(pkg, "_stream_ws", {})
+    monkeypatch.setattr(pkg, "_size_cache", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return state
+
+
+def attend():
+    q = torch.zeros(1, 40, 2, 64, dtype=torch.bfloat16)
+    pages = torch.zeros(2, 1, 16 * 72, dtype=torch.uint8)
+    return pkg.kv4_attend(q, pages, torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+
+
+def logprobs():
+    return pkg.token_logprobs(torch.zeros(2, 16), torch.zeros(2, dtype=torch.int32))
+
+
+def test_threads_on_one_stream_do_not_share_a_workspace_in_use(fake):
+    """A call's launches share one workspace; a call of another thread on the
+    same stream must not come between them with the same one."""
+    fake.hold = 0.005
+    threads = [threading.Thread(target=f) for f in (attend, logprobs) * 4]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    in_use = set()
+    for what, ws in fake.log:
+        if what == "in":
+            assert ws not in in_use
+            in_use.add(ws)
+        else:
+            in_use.remove(ws)
+    assert len(fake.log) == 16
+
+
+def test_one_workspace_a_stream_grown_on_demand(fake):
+    logprobs()
+    attend()
+    logprobs()
+    assert len({ws for _, ws in fake.log}) == 1   # both fit the first one
