@@ -730,10 +730,22 @@ class _StreamWorkspace:
         self.buf = None
 
 
+WORKSPACE_ZEROED = 8192   # include/dllm.h DLLM_WORKSPACE_ZEROED
+
+
 def _call(torch, fn, args, dev, stream, nbytes, workspace):
-    """fn(args, stream) with the caller's workspace, or the stream's own."""
+    """fn(args, stream) with the caller's workspace, or the stream's own.
+
+    A call that is being captured into a CUDA graph gets memory of the graph's
+    pool, cleared in the graph where it must be: replays then depend on no
+    other graph's or eager call's use of a workspace, and none of theirs on it."""
     if workspace is not None:
         args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        return fn(ctypes.byref(args), stream)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, WORKSPACE_ZEROED), dtype=torch.uint8, device=dev)
+        ws[:WORKSPACE_ZEROED].zero_()
+        args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
         return fn(ctypes.byref(args), stream)
     key = (dev.index, stream)
     own = _stream_ws.get(key) or _stream_ws.setdefault(key, _StreamWorkspace())
@@ -774,7 +786,8 @@ def token_logprobs(logits, tokens, *, V=None, top=0, rows=None, workspace=None):
     rows:      int32 [N] row of each entry, or None: entry i is row i
     top:       alternatives per entry, 0 to MAX_TOP
     workspace: uint8 CUDA tensor of dllm_logprobs_workspace_size bytes, zeroed
-               once; default: one kept for the current stream
+               once; default: one kept for the current stream (while a CUDA
+               graph is captured: one of the graph's own)
     Returns a dict: logprob and entropy (float32 [N]) and, with top, top_ids
     (int32 [N, top]) and top_logprobs (float32 [N, top]), largest first."""
     torch = _torch()
@@ -900,6 +913,7 @@ def kv4_attend(q, pages, table, lens, *, scale=None, prior=None, weights=None, w
     weights: float32 [n_pages, heads, page_size] or None: receives what every
              cached token was given by its head's queries, plus ``prior`` (the
              same tensor will do; None: 0)
+    workspace: as for token_logprobs, of dllm_kv4_attend_workspace_size bytes
     Returns a dict: out (bf16 like q, contiguous), lse (float32 [B, L,
     q_heads]) and, where given, weights."""
     torch = _torch()

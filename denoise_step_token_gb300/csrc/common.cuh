@@ -43,6 +43,7 @@ int sm_count();
 // lands on another's counters, whatever their shapes: one workspace may serve
 // both.
 constexpr int kJoinCounters = 2048;
+static_assert(kJoinCounters * sizeof(int) == DLLM_WORKSPACE_ZEROED, "what callers clear");
 
 // Let `kernel` use `bytes` of dynamic shared memory, once per device (`done`: a
 // static of the caller's, one per kernel; a race repeats the call).

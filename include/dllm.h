@@ -740,6 +740,7 @@ int dllm_loop_thresholds(const dllm_loop* loop, float* thr, int32_t* n);
  * are held in 32 bits and combined in a fixed order, so equal calls give
  * equal bits (the split of a row, and with it the last bits, depend on N).
  * Serves reports of sampled blocks: no gradient. */
+#define DLLM_WORKSPACE_ZEROED 8192   /* join counters at the start of these operators' workspaces */
 #define DLLM_MAX_TOP 32
 #define DLLM_DTYPE_BF16 0
 #define DLLM_DTYPE_F32 1
@@ -757,11 +758,11 @@ typedef struct dllm_logprobs_args {
     float* entropy;             /* device [N] out, or NULL */
     int32_t* top_ids;           /* device [N][top] out (NULL when top is 0) */
     float* top_logprobs;        /* device [N][top] out (NULL when top is 0) */
-    void* workspace;            /* device, >= dllm_logprobs_workspace_size() bytes, 256-byte aligned,
-                                   zero-filled before first use; every completed call leaves it ready
-                                   for the next; calls sharing it must be ordered on one stream, every
-                                   launch of one before the first of the next: threads that share it
-                                   take turns, a whole call each */
+    void* workspace;            /* device, >= dllm_logprobs_workspace_size() bytes, 256-byte aligned, its
+                                   first DLLM_WORKSPACE_ZEROED bytes zero before first use; every
+                                   completed call leaves it ready for the next; calls sharing it must
+                                   be ordered on one stream, every launch of one before the first of
+                                   the next: threads that share it take turns, a whole call each */
     size_t workspace_bytes;
 } dllm_logprobs_args;
 
@@ -870,7 +871,7 @@ typedef struct dllm_kv4_attend_args {
     float* lse;                 /* device [B][L][q_heads] out, or NULL without weights */
     const float* prior;         /* device [n_pages][heads][page_size], or NULL */
     float* weights;             /* device [n_pages][heads][page_size] out, or NULL */
-    void* workspace;            /* as dllm_logprobs_args: zero-filled before first use */
+    void* workspace;            /* as dllm_logprobs_args */
     size_t workspace_bytes;
 } dllm_kv4_attend_args;
 

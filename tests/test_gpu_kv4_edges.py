@@ -38,3 +38,56 @@ def test_calls_of_several_threads_on_one_stream(dllm):
         t.join()
     assert not wrong
     assert dllm.get_device_error(dev) == 0
+
+
+def operators(dllm, dev, seed):
+    """Calls of both operators that take a workspace, the attention at few and at
+    many rows, and their outputs."""
+    import torch
+    rng = np.random.default_rng(seed)
+    cache = Cache(rng, [3000, 700, 1], 2, 128, 32)
+    pages, table, lens = cache.upload(dev)
+    few, many = (bf16(rng.standard_normal((3, L, 14, 128)), dev) for L in (1, 16))
+    logits = bf16(rng.standard_normal((9, 40000)), dev)
+    tokens = torch.arange(9, dtype=torch.int32, device=dev)
+    w = torch.zeros(pages.shape[0], 2, 32, device=dev)
+
+    def call():
+        return [dllm.token_logprobs(logits, tokens, top=7), dllm.kv4_attend(few, pages, table, lens, weights=w),
+                dllm.kv4_attend(many, pages, table, lens)]
+    return call
+
+
+def test_captured_in_graphs(dllm):
+    """Graphs captured one after the other replay in any order, between eager
+    calls and side by side, with the bits of the eager calls."""
+    import torch
+    dev = torch.device("cuda", 0)
+    calls = [operators(dllm, dev, s) for s in (50, 51, 52)]
+    want = [[{k: t.clone() for k, t in o.items()} for o in c()] for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+
+    def same(i):
+        torch.cuda.synchronize()
+        for got, exp in zip(outs[i], want[i]):
+            for k in exp:
+                assert torch.equal(got[k], exp[k]), (i, k)
+                got[k].zero_()
+    for i in (2, 0, 1, 1, 0):
+        graphs[i].replay()
+        calls[1]()
+        same(i)
+    side = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for g, s in zip(graphs, side):
+        with torch.cuda.stream(s):
+            g.replay()
+    for i in range(3):
+        same(i)
+    assert dllm.get_device_error(dev) == 0

@@ -3,6 +3,7 @@
 The library is replaced by one that records the workspace each call is given,
 and the checks that ask for a CUDA device are taken out: what is tested is which
 memory a call gets, and who else may be using it."""
+import ctypes
 import threading
 import time
 from types import SimpleNamespace
@@ -73,3 +74,31 @@ def test_one_workspace_a_stream_grown_on_demand(fake):
     attend()
     logprobs()
     assert len({ws for _, ws in fake.log}) == 1   # both fit the first one
+
+
+def test_captured_calls_keep_to_their_graph(fake, monkeypatch):
+    """A graph replays with the memory that its capture saw.  So a captured call
+    leaves none for later calls, takes none of theirs, and clears its join
+    counters within the graph."""
+    zeroed = []
+
+    def seen(args):
+        raw = (ctypes.c_uint8 * args.workspace_bytes).from_address(args.workspace)
+        zeroed.append(not any(raw[:8192]))
+        raw[:8192] = b"\1" * 8192   # as if left by whatever ran before a replay
+    fake.seen = seen
+    before = attend() and fake.log[-1][1]
+    kept = torch.empty(0)
+    held = [kept]   # what the captured calls allocated, so that addresses cannot be used again
+    empty, zeros = torch.empty, torch.zeros
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: held.append(empty(*a, **k)) or held[-1])
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: held.append(zeros(*a, **k)) or held[-1])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    first = attend() and fake.log[-1][1]
+    second = logprobs() and fake.log[-1][1]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    fake.seen = None
+    after = attend() and fake.log[-1][1]
+    assert len({before, first, second}) == 3
+    assert after == before
+    assert zeroed == [True] * 3
