@@ -108,14 +108,16 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
             range = bf16x2_max_nan(range, __shfl_xor_sync(quad, range, 2));
             range = bf16x2_max_nan(range, 0u);
             const bool bad = (range & 0x7f80u) == 0x7f80u || (range & 0x7f800000u) == 0x7f800000u;
-            const float low = bf16_hi(range), wide = __fadd_rn(bf16_lo(range), low);   // low: negated
+            // halves: the whole range, up to twice bf16's largest, may pass 32 bits (what halving loses of subnormal
+            // numbers is far under the least step)
+            const float low = bf16_hi(range), wide = fmaf(bf16_lo(range), 0.5f, 0.5f * low);   // low: negated
             // wide / 15 correctly rounded (P. Markstein, "Computation of elementary functions on the IBM RISC
             // System/6000 processor", 1990), then up to 4 significant bits
             constexpr float k15 = 1.0f / 15.0f;
             float s = __fmul_rn(wide, k15);
             s = fmaf(fmaf(-s, 15.0f, wide), k15, s);
             s = __uint_as_float((__float_as_uint(s) + 0xfffffu) & ~0xfffffu);
-            s = fmaxf(s, kKv4MinStep);
+            s = fmaxf(2.0f * s, kKv4MinStep);
             constexpr float kGrid = 12288.0f, kInt = 12582912.0f;   // 1.5 * 2^13, 1.5 * 2^23
             float r = __frcp_rn(s);
             const float z = fminf((fmaf(low, r, kGrid) + (kInt - kGrid)) - kInt, 15.0f);

@@ -813,9 +813,11 @@ size_t dllm_kv4_page_bytes(int32_t page_size, int32_t head_dim);
  *   s = (max - min) / 15 rounded up to 4 significant bits, at least 2^-18;
  *   z = rint(-min / s), at most 15;  then s = min(s, 768);
  *   u = clamp(rint(x / s) + z, 0, 15)
- * (32-bit arithmetic, rint to even; what 768 is too small for saturates).  A
- * group holding an infinity or a NaN is written as NaN (codes 0).  k_out / v_out receive what the codes stand for, so that a
- * forward over the prompt may use the values later steps will see.
+ * (32-bit arithmetic in which no range of finite values overflows, rint to
+ * even; what 768 is too small for saturates).  A group holding an infinity or
+ * a NaN is written as NaN (codes 0).  k_out / v_out receive what the codes
+ * stand for, so that a forward over the prompt may use the values later steps
+ * will see.
  *   - strides in elements, multiples of 8, channels contiguous, base 16-byte
  *     aligned; k_out / v_out are contiguous [B][W][heads][D] (columns not
  *     written are left as they were).

@@ -5,9 +5,12 @@ by the operators' definitions."""
 import numpy as np
 import pytest
 
+import kv4_reference as ref
 from test_gpu_kv4 import Cache, bf16
 
 pytestmark = pytest.mark.gpu
+
+BIG = 3.3895313892515355e38   # bf16's largest
 
 
 def test_calls_of_several_threads_on_one_stream(dllm):
@@ -91,3 +94,32 @@ def test_captured_in_graphs(dllm):
     for i in range(3):
         same(i)
     assert dllm.get_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("low,high", [(-2e38, 2e38), (-3.3e38, 3.3e38), (-BIG, BIG), (-BIG, 1.0), (0.0, BIG),
+                                      (-1.0, BIG), (-BIG, 2e38), (-12000.0, 12000.0), (-20000.0, 300.0)])
+def test_write_ranges_that_saturate(dllm, low, high):
+    """Steps past their largest, up to ranges that no 32-bit number holds: codes,
+    parameters and values are those of the definition."""
+    import torch
+    dev = torch.device("cuda", 0)
+    rng = np.random.default_rng(40)
+    x = rng.uniform(-0.5, 0.5, (1, 8, 2, 2, 64)) * min(abs(high - low), 1e38)
+    x[..., 0::32], x[..., 17::32] = low, high
+    x[0, 3, :, :, 5] = 0.0
+    x = ref.from_bf16(ref.to_bf16(np.clip(x, low, high)))
+    pages, _ = dllm.kv4_pages(1, 2, 16, 64, dev)
+    t = bf16(x, dev)
+    out = [torch.empty((1, 8, 2, 64), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    zero = torch.zeros(1, dtype=torch.int32, device=dev)
+    dllm.kv4_write(t[:, :, 0], t[:, :, 1], pages, zero[None], zero, k_out=out[0], v_out=out[1])
+    assert dllm.get_device_error(dev) == 0
+    rows = np.zeros((2, 1, 2, 16, 64))
+    rows[:, 0, :, :8] = x[0].transpose(1, 2, 0, 3)
+    want = ref.pages_of(rows[0], rows[1], 16)
+    got = pages.cpu().numpy()
+    for at, size in ((0, 32), (16 * 32, 4), (16 * 36, 32), (16 * 68, 4)):   # the eight tokens written
+        np.testing.assert_array_equal(got[..., at:at + 8 * size], want[..., at:at + 8 * size])
+    vals = ref.values_of(want, 16, 64)
+    for i in range(2):
+        np.testing.assert_array_equal(out[i][0].float().cpu().numpy(), vals[i][0].transpose(1, 0, 2)[:8])
