@@ -606,7 +606,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_tile_kernel(const __grid_
                         for (int i = 1; i < 32; ++i) top[c] = fmaxf(top[c], __uint_as_float(x[c][i]));
                     }
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * rs;
-                    if (__any_sync(0xffffffffu, mx > m + kAbove)) {
+                    // lanes past the item's rows hold whatever was there: a move they asked for would change how
+                    // the rows beside them are rounded
+                    if (__any_sync(0xffffffffu, row < rows && mx > m + kAbove)) {
                         const float mn = fmaxf(m, mx - kBelow);
                         const float f = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
                         m = mn;

@@ -123,3 +123,34 @@ def test_write_ranges_that_saturate(dllm, low, high):
     vals = ref.values_of(want, 16, 64)
     for i in range(2):
         np.testing.assert_array_equal(out[i][0].float().cpu().numpy(), vals[i][0].transpose(1, 0, 2)[:8])
+
+
+def fill_shared_memory(dllm, dev, seed):
+    """Other kernels' data in every SM's shared memory: logits of any bits."""
+    import torch
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    bits = torch.randint(-2 ** 15, 2 ** 15, (2048, 30016), dtype=torch.int16, generator=gen, device=dev)
+    dllm.token_logprobs(bits.view(torch.bfloat16), torch.zeros(2048, dtype=torch.int32, device=dev))
+
+
+# rows that fill no warp: 56 and 100 (two streams share them), 234 of 256, and 700 in blocks of 234, 234 and 232
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L,H", [(8, 7), (25, 4), (39, 6), (100, 7)])
+def test_attend_equal_bits_with_rows_that_fill_no_warp(dllm, L, H, D):
+    """Equal calls give equal bits whatever ran before them, and whichever item
+    a CTA had before."""
+    import torch
+    dev = torch.device("cuda", 0)
+    rng = np.random.default_rng(41)
+    lens = rng.integers(100, 1500, 40)
+    cache = Cache(rng, lens, 1, D, 32)
+    q = rng.standard_normal((40, L, H, D)) * np.exp2(rng.integers(-3, 4, (40, L, H, 1)))
+    pages, table, tl = cache.upload(dev)
+    tq = bf16(q, dev)
+    want = dllm.kv4_attend(tq, pages, table, tl)
+    for i in range(8):
+        fill_shared_memory(dllm, dev, i)
+        got = dllm.kv4_attend(tq, pages, table, tl)
+        for k in want:
+            assert torch.equal(got[k], want[k]), (k, i)
