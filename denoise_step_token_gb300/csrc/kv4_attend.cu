@@ -28,46 +28,32 @@ namespace {
 // ---------------------------------------------------------------------------
 // Few rows: 16 rows per CTA, four warps with 16 tokens at a time
 // ---------------------------------------------------------------------------
-// Bound by memory: per token and head 1.125 D bytes against two m16n8k16 products
-// per 8 tokens and 16 channels.  Each warp streams tokens of its own: a ring of
-// six 16-token blocks (four bulk copies each: codes and parameters of keys and
-// values), 166 KB in flight per SM at three CTAs.  (With the loads in registers and
-// none ahead, 16 single tokens over caches of 20 K took 110 us.)  Codes go from the
-// ring straight to fragments: a thread widens what it feeds to the tensor cores.
-//
-// Column 2 t + p of an n8 tile of scores is token 4 p + t of its 8: the value rows
-// that a quad's threads read together are then neighbours, free of bank conflicts.
+// A thread loads the codes that it feeds to the tensor cores and widens them in
+// registers.  Bound by each warp's dependent chain (load, widen, score products,
+// vote, exponentials, widen, value products) with three warps per scheduler, not by
+// memory: 64 blocks of 32 rows over caches of 96 to 1280 tokens take 177 us (1.26
+// TB/s), 16 single tokens over caches of 8 to 33 K 109 us (1.47 TB/s).  The same
+// chain fed from rings of bulk copies, 166 KB in flight per SM, took 189 and 108 us.
 constexpr int kRowWarps = 4;
-constexpr int kRowStages = 6;
-constexpr uint64_t kRowWaitNs = 2000000000ull;   // any single wait gives up after 2 s
 
-template <int D>
-struct RowShape {
-    static constexpr uint32_t kCodes = 16 * (D / 2), kPars = 16 * (D / 16);
-    static constexpr uint32_t kBlock = 2 * (kCodes + kPars);
-    static constexpr uint32_t kRing = kRowWarps * kRowStages * kBlock;
-    static constexpr uint32_t kJoin = kRowWarps * 16 * (D + 4) * 4;   // over the ring, once it is read
-    static constexpr size_t kSmem = (kRing > kJoin ? kRing : kJoin) + 16;
-};
-
-// Codes of a block's values: tokens t, t + 4, t + 8, t + 12; channels [g D/8, (g+1) D/8).
+// V codes of 16 tokens: tokens 2t, 2t+1, 2t+8, 2t+9; channels [g D/8, (g+1) D/8).
 template <int D>
 struct ValueTile {
     static constexpr int kWords = D / 64;
     uint32_t w[4][kWords];
     uint32_t par[4];
-    __device__ __forceinline__ void load(const unsigned char* half, int g, int t) {
+    __device__ __forceinline__ void load(const uint8_t* half, int shift, int slot0, int g, int t) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int token = t + 4 * k;
-            const unsigned char* c = half + token * (D / 2) + g * (D / 16);
+            const int slot = slot0 + 2 * t + (k & 1) + (k >> 1) * 8;
+            const uint8_t* c = half + slot * (D / 2) + g * (D / 16);
             if constexpr (D == 128) {
-                const uint2 q = *reinterpret_cast<const uint2*>(c);
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(c));
                 w[k][0] = q.x; w[k][1] = q.y;
             } else {
-                w[k][0] = *reinterpret_cast<const uint32_t*>(c);
+                w[k][0] = __ldg(reinterpret_cast<const uint32_t*>(c));
             }
-            par[k] = reinterpret_cast<const uint16_t*>(half + RowShape<D>::kCodes + token * (D / 16))[g * (D / 8) / 32];
+            par[k] = __ldg(reinterpret_cast<const uint16_t*>(half + ((D / 2) << shift) + slot * (D / 16)) + g * (D / 8) / 32);
         }
     }
 };
@@ -77,10 +63,7 @@ template <int D>
 __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const __grid_constant__ AttendParams P) {
     constexpr int kNt = D / 8;    // n8 tiles of the output
     constexpr int kKs = D / 16;   // products along the channels
-    using T = RowShape<D>;
-    extern __shared__ __align__(128) unsigned char ring[];
-    float(*const s_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(ring);
-    __shared__ uint64_t s_bar[kRowWarps][kRowStages];
+    __shared__ float s_o[kRowWarps][16][D + 4];
     __shared__ float s_m[kRowWarps][16], s_l[kRowWarps][16];
     __shared__ int s_last;
     pdl_wait();
@@ -90,40 +73,6 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const _
     const int n = kv4_len(P.C, P.lens, b);
     const int blocks = (n + 15) >> 4;
     const int lo = (int)((long long)blocks * split / P.splits), hi = (int)((long long)blocks * (split + 1) / P.splits);
-    // this warp's blocks are lo + warp, + 4, ...: the i-th one's page number sits in lane i % 32
-    const int mine = max(hi - lo - warp + kRowWarps - 1, 0) / kRowWarps;
-    const int shift = P.C.page_shift, slot_mask = (1 << shift) - 1;
-    unsigned char* const stage0 = ring + warp * kRowStages * T::kBlock;
-    const uint64_t policy = l2_policy_evict_first();
-    int page_ids = 0;
-    auto copy = [&](int i) {   // start the copies of this warp's i-th block
-        if ((i & 31) == 0) {
-            const int at = i + lane;
-            page_ids = -1;
-            if (at < mine) page_ids = __ldg(P.C.table + (long long)b * P.C.max_pages + (((lo + warp + at * kRowWarps) * 16) >> shift));
-        }
-        int page = __shfl_sync(0xffffffffu, page_ids, i & 31);
-        if ((unsigned)page >= (unsigned)P.C.n_pages) {
-            if (lane == 0) set_error(P.C.err, DLLM_DEVERR_PAGE);
-            page = 0;   // some page's codes stand in
-        }
-        const uint32_t bar = smem_addr(&s_bar[warp][i % kRowStages]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, T::kBlock);
-        __syncwarp();
-        if (lane < 4) {   // keys' codes and parameters, values' codes and parameters
-            const int slot = ((lo + warp + i * kRowWarps) * 16) & slot_mask;
-            const uint8_t* src = P.C.pages + (page * P.C.page_bytes + (uint32_t)head * P.C.head_bytes) + (lane >> 1) * (P.C.head_bytes / 2);
-            const bool codes = (lane & 1) == 0;
-            bulk_g2s(smem_addr(stage0 + (i % kRowStages) * T::kBlock) + (lane >> 1) * (T::kCodes + T::kPars) + (codes ? 0 : T::kCodes),
-                     src + (codes ? slot * (D / 2) : ((D / 2) << shift) + slot * (D / 16)), codes ? T::kCodes : T::kPars, bar, policy);
-        }
-    };
-    if (lane == 0) {
-        for (int i = 0; i < kRowStages; ++i) mbar_init(smem_addr(&s_bar[warp][i]), 1);
-        mbar_fence_init();
-    }
-    __syncwarp();
-    for (int i = 0; i < min(mine, kRowStages); ++i) copy(i);
 
     // queries: rows g and g + 8 of the tile
     uint32_t qa[kKs][4];
@@ -162,22 +111,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const _
 #pragma unroll
     for (int k = 0; k < kNt; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    bool broken = false;
-    for (int i = 0; i < mine; ++i) {
-        const int j0 = (lo + warp + i * kRowWarps) * 16;
-        const unsigned char* in = stage0 + (i % kRowStages) * T::kBlock;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&s_bar[warp][i % kRowStages]), i / kRowStages & 1, kRowWaitNs))) {
-            if (lane == 0) set_error(P.C.err, DLLM_DEVERR_TIMEOUT);
-            broken = true;
-            break;
-        }
+    const int slot_mask = (1 << P.C.page_shift) - 1;
+    for (int blk = lo + warp; blk < hi; blk += kRowWarps) {
+        const int j0 = blk * 16;
+        const uint8_t* page = kv4_page(P.C, P.C.table, b, j0 >> P.C.page_shift, P.C.max_pages, head);
+        if (!page) page = P.C.pages;   // the error is recorded; results unspecified
+        const int slot0 = j0 & slot_mask;
         KeyTile<D> kt[2];
         ValueTile<D> vt;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) kt[u].read(in, T::kCodes, u * 8 + (g & 1) * 4 + (g >> 1), t);
-        vt.load(in + T::kCodes + T::kPars, g, t);
-        __syncwarp();   // the stage is read
-        if (i + kRowStages < mine) copy(i + kRowStages);
+        kt[0].load(page, P.C.page_shift, slot0 + g, t);
+        kt[1].load(page, P.C.page_shift, slot0 + 8 + g, t);
+        vt.load(page + P.C.head_bytes / 2, P.C.page_shift, slot0, g, t);
         float s[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -194,7 +138,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const _
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 s[u][e] *= rs[e >> 1];
-                if (ragged && j0 + u * 8 + (e & 1) * 4 + t >= n) s[u][e] = -INFINITY;
+                if (ragged && j0 + u * 8 + 2 * t + (e & 1) >= n) s[u][e] = -INFINITY;
                 top[e >> 1] = fmaxf(top[e >> 1], s[u][e]);
             }
         if (__any_sync(0xffffffffu, top[0] > m[0] + kAbove || top[1] > m[1] + kAbove)) {
@@ -223,14 +167,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const _
                 l[h] += p0 + p1;
                 pa[h + 2 * u] = pack_h2(p0, p1);
             }
-        // values: parameters of tokens (t, t + 4) and (t + 8, t + 12) side by side; past the end they make zeros
+        // values: parameters of tokens (2t, 2t+1) and (2t+8, 2t+9) side by side; past the end they make zeros
         Kv4Scale vs[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             vs[u] = kv4_scale(vt.par[2 * u] | (vt.par[2 * u + 1] << 16));
             if (ragged) {
-                const int j = j0 + u * 8 + t;
-                const uint32_t keep = (j < n ? 0xffffu : 0u) | (j + 4 < n ? 0xffff0000u : 0u);
+                const int j = j0 + u * 8 + 2 * t;
+                const uint32_t keep = (j < n ? 0xffffu : 0u) | (j + 1 < n ? 0xffff0000u : 0u);
                 vs[u].s &= keep;
                 vs[u].c &= keep;
             }
@@ -249,9 +193,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_attend_rows_kernel(const _
         }
     }
 
-    // the warps' results, then the CTA's, over the rings
-    if (broken) __nanosleep(1000000);   // copies in flight land first
-    __syncthreads();
+    // the warps' results, then the CTA's
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -529,11 +471,8 @@ extern "C" int dllm_kv4_attend(const dllm_kv4_attend_args* a, void* stream) {
     cudaStream_t s = as_stream(stream);
     if (P.Q.rows <= kFewRows) {
         P.partial = reinterpret_cast<float*>(ws);
-        static SmemOnce done128, done64;
-        auto kernel = D == 128 ? kv4_attend_rows_kernel<128> : kv4_attend_rows_kernel<64>;
-        const size_t smem = D == 128 ? RowShape<128>::kSmem : RowShape<64>::kSmem;
-        DLLM_CUDA_TRY(allow_smem(kernel, smem, D == 128 ? done128 : done64));
-        DLLM_CUDA_TRY(launch_dependent(kernel, dim3(P.splits, H * P.tiles, B), dim3(kRowWarps * 32), smem, s, P));
+        DLLM_CUDA_TRY(launch_dependent(D == 128 ? kv4_attend_rows_kernel<128> : kv4_attend_rows_kernel<64>,
+                                       dim3(P.splits, H * P.tiles, B), dim3(kRowWarps * 32), 0, s, P));
     } else {
         P.partial = reinterpret_cast<float*>(ws + sizeof(TilePlan) + max_items(a->cache, P.Q.rows) * sizeof(TileItem));
         rc = launch_attend_tiles(P, D, s);

@@ -61,18 +61,6 @@ struct KeyTile {
         }
         par = __ldg(reinterpret_cast<const uint16_t*>(page + ((D / 2) << shift) + slot * (D / 16)) + t * (D / 4) / 32);
     }
-    // The same of a block in shared memory, its parameters `pars` bytes on.
-    __device__ __forceinline__ void read(const unsigned char* block, uint32_t pars, int token, int t) {
-        const unsigned char* c = block + token * (D / 2) + t * (D / 8);
-        if constexpr (D == 128) {
-            const uint4 q = *reinterpret_cast<const uint4*>(c);
-            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-        } else {
-            const uint2 q = *reinterpret_cast<const uint2*>(c);
-            w[0] = q.x; w[1] = q.y;
-        }
-        par = reinterpret_cast<const uint16_t*>(block + pars + token * (D / 16))[t * (D / 4) / 32];
-    }
     // b0, b1 of the D/16 products along the channels
     __device__ __forceinline__ void widen(uint32_t (&b)[D / 16][2]) const {
         const Kv4Scale p = kv4_scale(kv4_splat(par));
