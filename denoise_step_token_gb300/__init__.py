@@ -740,6 +740,8 @@ def _call(torch, fn, args, dev, stream, nbytes, workspace):
     pool, cleared in the graph where it must be: replays then depend on no
     other graph's or eager call's use of a workspace, and none of theirs on it."""
     if workspace is not None:
+        if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous uint8 tensor on the other tensors' device")
         args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
         return fn(ctypes.byref(args), stream)
     if torch.cuda.is_current_stream_capturing():

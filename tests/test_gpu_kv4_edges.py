@@ -154,3 +154,26 @@ def test_attend_equal_bits_with_rows_that_fill_no_warp(dllm, L, H, D):
         got = dllm.kv4_attend(tq, pages, table, tl)
         for k in want:
             assert torch.equal(got[k], want[k]), (k, i)
+
+
+def test_refused_workspaces(dllm):
+    """A workspace on the host, of another type, misaligned or in pieces is
+    refused before anything is launched."""
+    import torch
+    dev = torch.device("cuda", 0)
+    pages, _ = dllm.kv4_pages(2, 1, 16, 64, dev)
+    table = torch.zeros(1, 2, dtype=torch.int32, device=dev)
+    one = torch.ones(1, dtype=torch.int32, device=dev)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device=dev)
+    n = 64 << 20
+    good = torch.zeros(n, dtype=torch.uint8, device=dev)
+    calls = (lambda w: dllm.kv4_attend(q, pages, table, one, workspace=w),
+             lambda w: dllm.token_logprobs(torch.zeros(1, 64, device=dev), one, workspace=w))
+    for call in calls:
+        call(good)
+        for bad in (torch.zeros(n, dtype=torch.uint8), good[::2], torch.zeros(n // 4, device=dev)):
+            with pytest.raises((ValueError, TypeError)):
+                call(bad)
+        with pytest.raises(dllm.DllmError):
+            call(good[16:])
+    assert dllm.get_device_error(dev) == 0

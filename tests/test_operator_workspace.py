@@ -102,3 +102,16 @@ def test_captured_calls_keep_to_their_graph(fake, monkeypatch):
     assert len({before, first, second}) == 3
     assert after == before
     assert zeroed == [True] * 3
+
+
+def test_refused_workspaces(fake):
+    """Memory that a kernel cannot use as its workspace never reaches the
+    library: another device's, of another type, or in pieces."""
+    logits, tokens = torch.zeros(2, 16), torch.zeros(2, dtype=torch.int32)
+    pkg.token_logprobs(logits, tokens, workspace=torch.zeros(9000, dtype=torch.uint8))
+    assert len(fake.log) == 2
+    for bad in (torch.zeros(9000, dtype=torch.uint8, device="meta"), torch.zeros(9000),
+                torch.zeros(18000, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            pkg.token_logprobs(logits, tokens, workspace=bad)
+    assert len(fake.log) == 2
