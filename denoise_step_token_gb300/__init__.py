@@ -836,6 +836,15 @@ def kv4_pages(n_pages, heads, page_size, head_dim, device):
             torch.zeros((n_pages, heads, page_size), dtype=torch.float32, device=device))
 
 
+def _kv4_page_size(pages, head_dim):
+    """Tokens of the pool's pages, as their bytes have it."""
+    if pages.dim() != 3:
+        raise TypeError("pages must be uint8 [n_pages, heads, bytes]")
+    if head_dim < 1:
+        raise ValueError("head_dim must be 64 or 128")
+    return pages.shape[2] // (head_dim + head_dim // 8)
+
+
 def _kv4_cache(torch, pages, table, page_size, head_dim):
     if pages.dtype != torch.uint8 or pages.dim() != 3:
         raise TypeError("pages must be uint8 [n_pages, heads, bytes]")
@@ -885,7 +894,7 @@ def kv4_write(k, v, pages, table, pos, *, first=None, count=None, k_out=None, v_
     vb, vt, vh, vc = v.stride()
     if kc != 1 or vc != 1:
         raise ValueError("the channels of k and v must be contiguous")
-    cache = _kv4_cache(torch, pages, table, pages.shape[2] // (D + D // 8), D)
+    cache = _kv4_cache(torch, pages, table, _kv4_page_size(pages, D), D)
     if cache.B != B or cache.heads != heads:
         raise ValueError("k, v, pages and table disagree about requests or heads")
     ko = vo = None
@@ -930,7 +939,7 @@ def kv4_attend(q, pages, table, lens, *, scale=None, prior=None, weights=None, w
     qb, ql, qh, qc = q.stride()
     if qc != 1:
         raise ValueError("the channels of q must be contiguous")
-    page_size = pages.shape[2] // (D + D // 8)
+    page_size = _kv4_page_size(pages, D)
     cache = _kv4_cache(torch, pages, table, page_size, D)
     if cache.B != B:
         raise ValueError("q and table disagree about the requests")
@@ -964,7 +973,10 @@ def kv4_evict(pages, weights, table, lens, keep, dst_table, *, recent=0):
     torch = _torch()
     dev = pages.device
     _check_tensors(torch, dev, pages, weights, table, lens, keep, dst_table)
-    if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[:2] != pages.shape[:2]:
+    if pages.dim() != 3:
+        raise TypeError("pages must be uint8 [n_pages, heads, bytes]")
+    if (weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[:2] != pages.shape[:2]
+            or weights.shape[2] < 1):
         raise TypeError("weights must be float32 [n_pages, heads, page_size]")
     page_size = weights.shape[2]
     cache = _kv4_cache(torch, pages, table, page_size, pages.shape[2] // page_size * 8 // 9)

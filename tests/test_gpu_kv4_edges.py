@@ -177,3 +177,26 @@ def test_refused_workspaces(dllm):
         with pytest.raises(dllm.DllmError):
             call(good[16:])
     assert dllm.get_device_error(dev) == 0
+
+
+def test_refused_shapes(dllm):
+    """Wrong numbers of dimensions, and none at all, are refused by name."""
+    import torch
+    dev = torch.device("cuda", 0)
+    pages, weights = dllm.kv4_pages(2, 1, 16, 64, dev)
+    table = torch.zeros(1, 2, dtype=torch.int32, device=dev)
+    one = torch.ones(1, dtype=torch.int32, device=dev)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device=dev)
+    for flat in (pages[0], pages.reshape(-1)):
+        with pytest.raises((TypeError, ValueError)):
+            dllm.kv4_attend(q, flat, table, one)
+        with pytest.raises((TypeError, ValueError)):
+            dllm.kv4_write(q, q, flat, table, one)
+        with pytest.raises((TypeError, ValueError)):
+            dllm.kv4_evict(flat, weights, table, one, one, table)
+    with pytest.raises((TypeError, ValueError)):
+        dllm.kv4_attend(q[..., :0], pages, table, one)
+    with pytest.raises((TypeError, ValueError)):
+        dllm.kv4_write(q[..., :0], q[..., :0], pages, table, one)
+    with pytest.raises((TypeError, ValueError)):
+        dllm.kv4_evict(pages, weights[:, :, :0].contiguous(), table, one, one, table)
