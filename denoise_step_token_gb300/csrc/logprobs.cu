@@ -119,16 +119,21 @@ struct Sums {
     float m, z, t;
 };
 
-// c a - c b as the sums hold it (c m is rounded once, the same everywhere).
+// Sums under a maximum within kPlain are formed with c m rounded once, the same
+// everywhere: their y are c (x - m) + offset2(m).  Beyond it they are c (x - m).
+__device__ __forceinline__ float offset2(float m) {
+    return fabsf(m) <= kPlain ? fmaf(m, kLog2e, -__fmul_rn(m, kLog2e)) : 0.0f;
+}
+// What takes sums under a to sums under b: c a - c b as they hold it.
 __device__ __forceinline__ float diff2(float a, float b) {
     return fabsf(b) <= kPlain && fabsf(a) <= kPlain ? __fsub_rn(__fmul_rn(a, kLog2e), __fmul_rn(b, kLog2e))
-                                                    : (a - b) * kLog2e;
+                                                    : fmaf(a - b, kLog2e, offset2(b) - offset2(a));
 }
 // ln p of one value, lz = log2 z: by the y the sums were formed with where c x
 // is sure to be finite.
 __device__ __forceinline__ float log_prob(float x, float m, float lz) {
     if (fabsf(m) <= kPlain && fabsf(x) <= kPlain) return (fmaf(x, kLog2e, -__fmul_rn(m, kLog2e)) - lz) * kLn2;
-    return (x - m) - lz * kLn2;
+    return (x - m) - (lz - offset2(m)) * kLn2;
 }
 
 // (a, then b): sums over both ranges.
