@@ -176,11 +176,11 @@ __device__ __forceinline__ void load_round(uint4 (&q)[kVec], const unsigned char
     constexpr int per = Round<T>::kPer;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) q[i] = reinterpret_cast<const uint4*>(stage)[i * kThreads + (int)threadIdx.x];
-    if (v0 + kThreads * kVec * per > V) {
+    if (V - v0 < kThreads * kVec * per) {
         const uint32_t ninf = Round<T>::kNegInfWord;
 #pragma unroll
         for (int i = 0; i < kVec; ++i)   // not copied: whatever the ring held
-            if (v0 + (i * kThreads + (int)threadIdx.x) * per >= V) q[i] = make_uint4(ninf, ninf, ninf, ninf);
+            if ((i * kThreads + (int)threadIdx.x) * per >= V - v0) q[i] = make_uint4(ninf, ninf, ninf, ninf);
     }
 }
 
@@ -190,7 +190,7 @@ __device__ __forceinline__ void mask_round(uint4 (&q)[kVec], int v0, int V) {
     constexpr int per = Round<T>::kPer;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const int n = V - (v0 + (i * kThreads + (int)threadIdx.x) * per);   // valid values of this load
+        const int n = V - v0 - (i * kThreads + (int)threadIdx.x) * per;   // valid values of this load
         if (n >= per) continue;
         uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
@@ -274,7 +274,7 @@ __device__ __forceinline__ void append(Shared& sh, u64* list, const unsigned cha
             float x;
             if constexpr (sizeof(T) == 2) x = __uint_as_float((uint32_t)reinterpret_cast<const T*>(stage)[at] << 16);
             else x = reinterpret_cast<const T*>(stage)[at];
-            if (v0 + at < V && x >= low) {
+            if (at < V - v0 && x >= low) {
                 const u64 key = make_key(x, v0 + at);
                 if (key > above) {
                     const int slot = atomicAdd(&sh.count, 1);
@@ -294,7 +294,7 @@ __device__ __noinline__ int select_slow(Shared& sh, u64* list, u64* to, const T*
     int* const hist = reinterpret_cast<int*>(to);   // 256 counts, until the sort
     if (tid == 0) sh.count = 0;
     if (n <= top) {
-        for (int v = v0 + tid; v < v1; v += kThreads) list[v - v0] = make_key(load_value(row, v), v);
+        for (int i = tid; i < n; i += kThreads) list[i] = make_key(load_value(row, v0 + i), v0 + i);
         sync_streams();
         return keep_best(list, to, n, top);
     }
@@ -303,8 +303,8 @@ __device__ __noinline__ int select_slow(Shared& sh, u64* list, u64* to, const T*
     for (int shift = 24; shift >= (sizeof(T) == 2 ? 16 : 0); shift -= 8) {
         for (int k = tid; k < 256; k += kThreads) hist[k] = 0;
         sync_streams();
-        for (int v = v0 + tid; v < v1; v += kThreads) {
-            const uint32_t k = ordered(load_value(row, v));
+        for (uint32_t i = tid; i < (uint32_t)n; i += kThreads) {
+            const uint32_t k = ordered(load_value(row, v0 + i));
             if (shift == 24 || ((k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[(k >> shift) & 255], 1);
         }
         sync_streams();
@@ -322,11 +322,12 @@ __device__ __noinline__ int select_slow(Shared& sh, u64* list, u64* to, const T*
     // of the values with this prefix (bf16: equal ones) the first `need` tokens
     constexpr uint32_t kBits = sizeof(T) == 2 ? 0xffff0000u : 0xffffffffu;
     int before = 0;
-    for (int w0 = v0; w0 < v1; w0 += kThreads) {
-        const int v = w0 + tid;
-        const float x = v < v1 ? load_value(row, v) : 0.0f;
+    for (uint32_t w0 = 0; w0 < (uint32_t)n; w0 += kThreads) {
+        const uint32_t i = w0 + tid;
+        const int v = v0 + (int)i;
+        const float x = i < (uint32_t)n ? load_value(row, v) : 0.0f;
         const uint32_t k = ordered(x) & kBits;
-        const bool eq = v < v1 && k == prefix;
+        const bool eq = i < (uint32_t)n && k == prefix;
         const unsigned bal = __ballot_sync(0xffffffffu, eq);
         if (lane == 0) hist[warp] = __popc(bal);
         sync_streams();
@@ -335,7 +336,7 @@ __device__ __noinline__ int select_slow(Shared& sh, u64* list, u64* to, const T*
             here += w < warp ? hist[w] : 0;
             before += hist[w];
         }
-        if (v < v1 && (k > prefix || (eq && here + __popc(bal & ((1u << lane) - 1u)) < need)))
+        if (i < (uint32_t)n && (k > prefix || (eq && here + __popc(bal & ((1u << lane) - 1u)) < need)))
             list[atomicAdd(&sh.count, 1)] = make_key(x, v);   // `top` in all
         sync_streams();
     }
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) logprob_kernel(const __
                     break;
                 }
                 const int v0 = rd * kRound;
-                const uint32_t bytes = r < 0 ? 0u : (uint32_t)min(kRoundBytes, (uint32_t)((P.V - v0 + per - 1) / per) * 16u);
+                const uint32_t bytes = r < 0 ? 0u : min(kRoundBytes / 16, (uint32_t)((P.V - v0 - 1) / per + 1)) * 16u;
                 mbar_arrive_expect_tx(smem_addr(&sh.full[k]), bytes);
                 if (bytes)
                     bulk_g2s(smem_addr(ring + k * kRoundBytes), static_cast<const T*>(P.logits) + r * P.ldv + v0, bytes,
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) logprob_kernel(const __
                 if (lane == 0) mbar_arrive(smem_addr(&sh.empty[k]));
                 continue;
             }
-            if (v0 + kRound > P.V) mask_round<T>(q, v0, P.V);
+            if (P.V - v0 < kRound) mask_round<T>(q, v0, P.V);
             const float bm = round_max<T>(q);
             uint32_t fl = 0;
             if constexpr (kTop) {
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) logprob_kernel(const __
         if (kTop && row) {
             sync_streams();
             if (sh.over) {
-                kept = select_slow<T>(sh, sh.lists[in_use], sh.lists[in_use ^ 1], row, rd0 * kRound, min(rd1 * kRound, P.V), P.top);
+                kept = select_slow<T>(sh, sh.lists[in_use], sh.lists[in_use ^ 1], row, rd0 * kRound, rd1 < P.rounds ? rd1 * kRound : P.V, P.top);
                 in_use ^= 1;
                 sync_streams();
             }
@@ -693,7 +694,7 @@ extern "C" int dllm_logprobs(const dllm_logprobs_args* a, void* stream) {
     P.N = a->N;
     P.V = a->V;
     P.top = a->top;
-    P.rounds = (a->V + round_values(a->dtype) - 1) / round_values(a->dtype);
+    P.rounds = (a->V - 1) / round_values(a->dtype) + 1;
     P.total = (long long)a->N * P.rounds;
     P.ctas = (int)std::min<long long>(P.total, std::min(sms * kPerSm, kMaxCtas));
     P.ldv = a->ldv;

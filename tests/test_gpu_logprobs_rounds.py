@@ -5,8 +5,8 @@ Tolerance: that of test_gpu_logprobs.py, 1e-5 max(1, |value|)."""
 import numpy as np
 import pytest
 
-
-from test_gpu_logprobs import check
+import kv4_reference as ref
+from test_gpu_logprobs import TOL, check
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +24,28 @@ def test_maxima_where_the_arithmetic_changes(dllm, size, sign):
     x[2] += rng.uniform(-1, 1, V).astype(np.float32)
     x[3] = np.sort(x[2])
     check(dllm, x, [3, V - 1, 17, 0], 4, "f32", 40016)
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 2 ** 30 + 1003), ("bf16", 2 ** 31 - 1)])
+def test_vocabularies_near_the_largest(dllm, dtype, V):
+    """Byte counts and ends of rounds that pass 32 bits: one row of 4 GB."""
+    import torch
+    dev = torch.device("cuda", 0)
+    ldv = -(-V // 8) * 8
+    logits = torch.full((1, ldv), float("-inf"), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device=dev)
+    logits[0, V:] = float("nan")
+    at = np.array([0, 5, 1500, 2040, 4095, 4096, V // 3, V - 4097, V - 700, V - 1])
+    vals = np.array([1.5, 3.0, 7.0, -2.0, 6.5, 0.25, 2.0, 4.0, 5.0, 6.0], dtype=np.float32)
+    logits[0, torch.from_numpy(at).to(dev)] = torch.from_numpy(vals).to(dev).to(logits.dtype)
+    out = dllm.token_logprobs(logits, torch.tensor([1500], dtype=torch.int32, device=dev), V=V, top=12)
+    got = {k: v.cpu().numpy()[0] for k, v in out.items()}
+    lp, ent, order, tlp = ref.logprobs(vals, 2, 10)
+    np.testing.assert_allclose(got["logprob"], lp, rtol=TOL, atol=TOL)
+    np.testing.assert_allclose(got["entropy"], ent, rtol=TOL, atol=TOL)
+    np.testing.assert_array_equal(got["top_ids"][:10], at[order])
+    np.testing.assert_allclose(got["top_logprobs"][:10], tlp, rtol=TOL, atol=TOL)
+    # the rest are the lowest tokens of probability 0
+    rest = [v for v in range(12) if v not in at][:2]
+    np.testing.assert_array_equal(got["top_ids"][10:], rest)
+    assert np.isneginf(got["top_logprobs"][10:]).all()
+    assert dllm.get_device_error(dev) == 0
