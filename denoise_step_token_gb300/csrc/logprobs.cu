@@ -649,6 +649,8 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) logprob_kernel(const __
         }
         sync_streams();   // the list and the parts are free
     }
+    // after a wait that gave up: copies still in flight land in this CTA's memory, not in its successor's
+    if (*(volatile int*)&sh.abort) __nanosleep(1000000);
 }
 
 inline int round_values(int dtype) { return kThreads * kVec * (dtype == DLLM_DTYPE_F32 ? 4 : 8); }
