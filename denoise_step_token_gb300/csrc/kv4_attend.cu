@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv4_weights_kernel(const __
 // Host
 // ---------------------------------------------------------------------------
 constexpr int kMaxSlots = 4096;   // splits of all units (request, head, tile) in a call
+constexpr int kMaxSplits = 64;    // of one unit
 constexpr int kFewRows = 32;      // up to this many rows per key/value head: kv4_attend_rows_kernel
 
 // Splits of a unit's tokens: enough that every SM has its three resident CTAs
@@ -397,7 +398,7 @@ inline int pick_splits(long long units, int max_tokens, int sms) {
     long long s = ((long long)sms * 6 + units - 1) / units;
     s = std::min<long long>(s, (max_tokens + 255) / 256);
     s = std::min<long long>(s, kMaxSlots / units);
-    return (int)std::max<long long>(std::min<long long>(s, 64), 1);
+    return (int)std::max<long long>(std::min<long long>(s, kMaxSplits), 1);
 }
 
 // Blocks of rows of a key/value head, and the items a plan may hold: every unit
@@ -423,7 +424,10 @@ extern "C" size_t dllm_kv4_attend_workspace_size(const dllm_kv4_cache* c, int32_
     if (check_rows(*c, L, q_heads) != DLLM_OK) return 0;
     const int rows = L * (q_heads / c->heads);
     size_t n = size_t(kJoinCounters) * 4;
-    if (rows <= kFewRows) return n + size_t(kMaxSlots) * 16 * (c->head_dim + 2) * 4;
+    if (rows <= kFewRows) {   // no more for fewer units, or a shorter table: one workspace serves a shrinking batch
+        const size_t units = size_t(std::max(c->B, 1)) * c->heads * ((rows + 15) / 16);
+        return n + std::min(units * kMaxSplits, size_t(kMaxSlots)) * 16 * (c->head_dim + 2) * 4;
+    }
     n += sizeof(TilePlan) + max_items(*c, rows) * sizeof(TileItem);
     return n + size_t(2 * kMaxCtas) * kTileRows * (c->head_dim + 2) * 4;
 }

@@ -877,7 +877,8 @@ typedef struct dllm_kv4_attend_args {
     size_t workspace_bytes;
 } dllm_kv4_attend_args;
 
-/* Workspace bytes (0 if invalid). */
+/* Workspace bytes (0 if invalid): no more for a smaller B or L, and the same
+ * for any max_pages. */
 size_t dllm_kv4_attend_workspace_size(const dllm_kv4_cache* cache, int32_t L, int32_t q_heads);
 
 int dllm_kv4_attend(const dllm_kv4_attend_args* args, void* stream);

@@ -115,3 +115,20 @@ def test_refused_workspaces(fake):
         with pytest.raises(ValueError):
             pkg.token_logprobs(logits, tokens, workspace=bad)
     assert len(fake.log) == 2
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_workspace_follows_the_batch(D):
+    """A token's call asks for what its units (16 rows of a request's head) can
+    be cut into, 64 pieces each and 4096 in all; a smaller batch never for more."""
+    size = lambda B, heads, L, q_heads: int(pkg.load().dllm_kv4_attend_workspace_size(  # noqa: E731
+        ctypes.byref(pkg.Kv4Cache(9, heads, 32, D, B, 7, None, None)), L, q_heads))
+    piece = 16 * (D + 2) * 4
+    assert size(1, 1, 1, 1) == 8192 + 64 * piece
+    assert size(0, 1, 1, 8) == size(1, 1, 1, 8) == 8192 + 64 * piece
+    assert size(3, 2, 5, 8) == 8192 + 3 * 2 * 2 * 64 * piece
+    assert size(64, 8, 1, 8) == size(4096, 8, 1, 8) == 8192 + 4096 * piece
+    for heads, group in ((1, 1), (4, 7)):
+        by_batch = [size(B, heads, 1, heads * group) for B in (1, 2, 15, 16, 17, 200, 5000)]
+        by_rows = [size(6, heads, L, heads * group) for L in (1, 2, 4, 5, 32, 100, 1024)]
+        assert by_batch == sorted(by_batch) and by_rows == sorted(by_rows)
