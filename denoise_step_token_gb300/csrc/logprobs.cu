@@ -11,7 +11,7 @@
 // of what an SM can issue while its share of memory arrives), or, for a row or
 // two, the launch and the joins.
 //
-// Split.  All entries' rounds (a round: 256 threads x 64 bytes of a row) are one
+// Split.  All entries' rounds (a round: 128 threads x 64 bytes of a row) are one
 // stream, cut evenly over the CTAs, six per SM.  A fifth warp keeps up to four
 // rounds of its CTA in flight as bulk copies (8 KB each, 190 KB per SM: under
 // load a copy lands about 2.8 us after its issue, and with the next round's loads

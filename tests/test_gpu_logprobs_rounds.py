@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import kv4_reference as ref
-from test_gpu_logprobs import TOL, check
+from test_gpu_logprobs import TOL, check, rows, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -48,4 +48,34 @@ def test_vocabularies_near_the_largest(dllm, dtype, V):
     rest = [v for v in range(12) if v not in at][:2]
     np.testing.assert_array_equal(got["top_ids"][10:], rest)
     assert np.isneginf(got["top_logprobs"][10:]).all()
+    assert dllm.get_device_error(dev) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["peaked", "ties", "equal", "ascending", "masked", "lowest", "signed_zero"])
+@pytest.mark.parametrize("top", [0, 3, 32])
+def test_whole_rows_of_several_rounds(dllm, dtype, kind, top):
+    """At most six CTAs run on an SM, so with 18 rows to each SM a CTA has two
+    whole rows or more, 8 (bf16) or 15 (f32) rounds each: lists, floors and sums
+    are used again from row to row."""
+    import torch
+    dev = torch.device("cuda", 0)
+    V = 30011
+    n = 18 * torch.cuda.get_device_properties(dev).multi_processor_count
+    x = rows(np.random.default_rng(6), 5, V, dtype, kind)
+    rng = np.random.default_rng(7)
+    idx = rng.integers(0, 5, n)
+    tokens = rng.integers(0, V, 5)
+    out = dllm.token_logprobs(upload(x, dtype, 30016, dev), torch.tensor(tokens[idx], dtype=torch.int32, device=dev), V=V,
+                              top=top, rows=torch.tensor(idx, dtype=torch.int32, device=dev))
+    got = {k: v.cpu().numpy() for k, v in out.items()}
+    for r in range(5):
+        mine = idx == r
+        lp, ent, ids, tlp = ref.logprobs(x[r], tokens[r], top)
+        want = {"logprob": lp, "entropy": ent}
+        if top:
+            np.testing.assert_array_equal(got["top_ids"][mine], np.broadcast_to(ids, (mine.sum(), top)))
+            want["top_logprobs"] = tlp
+        for name, w in want.items():
+            np.testing.assert_allclose(got[name][mine], np.broadcast_to(w, got[name][mine].shape), rtol=TOL, atol=TOL)
     assert dllm.get_device_error(dev) == 0
