@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import kv4_reference as ref
-from test_gpu_kv4 import Cache, bf16
+from test_gpu_kv4 import Cache, bf16, check_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +200,14 @@ def test_refused_shapes(dllm):
         dllm.kv4_write(q[..., :0], q[..., :0], pages, table, one)
     with pytest.raises((TypeError, ValueError)):
         dllm.kv4_evict(pages, weights[:, :, :0].contiguous(), table, one, one, table)
+
+
+# query rows per key/value head at the edges of the kernels' rules, with the tokens' weights
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L,H", [(8, 4), (11, 3), (16, 7), (32, 4), (43, 3), (32, 8), (33, 8), (64, 8), (100, 7)])
+def test_attend_rows_at_the_rules_edges(dllm, L, H, D):
+    """32, 33, 112, 128, 129, 256, 264, 512 and 700 rows."""
+    rng = np.random.default_rng(42)
+    lens = [0, 1, 128, 129, 400, 1300]
+    cache = Cache(rng, lens, 1, D, 32)
+    check_attend(dllm, cache, rng.standard_normal((len(lens), L, H, D)), weights=True)
