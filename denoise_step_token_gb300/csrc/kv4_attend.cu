@@ -389,10 +389,20 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv4_weights_kernel(const __
 // ---------------------------------------------------------------------------
 constexpr int kMaxSlots = 4096;   // splits of all units (request, head, tile) in a call
 constexpr int kMaxSplits = 64;    // of one unit
-constexpr int kFewRows = 32;      // up to this many rows per key/value head: kv4_attend_rows_kernel
+// Up to this many rows per key/value head: kv4_attend_rows_kernel, then the tile
+// kernels.  64 requests of 8 heads and 96 to 1280 tokens: 16 rows 51 us (tiles 61),
+// 32 rows 60 (61), 40 rows 79 (63).  With weights the tiles are ahead from 24 rows
+// on (94 against 110), and over 4 requests of 20 to 33 K tokens and 4 heads at any
+// number (8 rows: 61 against 69).
+constexpr int kFewRows = 32;
 
 // Splits of a unit's tokens: enough that every SM has its three resident CTAs
-// a few times over, none under 256 tokens.
+// twice over, none under 256 tokens.  One row of seven heads a key/value head, us:
+//   six CTAs an SM (three, twelve): 32 requests of 4 heads and 8 to 33 K tokens 166
+//   (192, 168), 8 such requests 65 (61, 87), 64 of 8 heads and up to 400 tokens 32
+//   (16, 32);
+//   256 tokens (128, 512): one request of 4 heads and up to 1280 tokens 11.0 (11.3,
+//   12.2), 8 of them 14 (17, 13), 32 of up to 400 tokens 15 (18, 8).
 inline int pick_splits(long long units, int max_tokens, int sms) {
     if (units > kJoinCounters) return 1;
     long long s = ((long long)sms * 6 + units - 1) / units;

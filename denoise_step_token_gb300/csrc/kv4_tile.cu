@@ -26,18 +26,21 @@
 // are joined at the end.  While one stream's softmax runs the tensor cores serve
 // the other.  Softmax weights go back to TMEM over the scores they came from, in
 // fp16, as the A operand of the product with the values.  The two products of a
-// tile and stream cost 4 x 128 x 128 x D operations whatever the rows, so the
-// kernel is bound by the tensor cores (2 x 512 cycles per tile and stream at
-// D = 128) when the rows fill the streams.
+// tile and stream cost 4 x 128 x 128 x D operations whatever the rows: 2 x 512
+// cycles of the tensor cores per tile and stream at D = 128.
 //
 // Codes are copied to shared memory by the TMA engine, read from there and
 // widened: 16 bytes of codes make 64 bytes of tile.  Six half-tiles of codes, 55
-// KB, are in flight per SM; held in registers one tile ahead instead (18 KB) they
-// took 3900 cycles a tile in the weights' kernel, the memory's latency, against
-// the 900 of its products.  The issuing thread orders the tiles' generic writes
+// KB, are in flight per SM.  The issuing thread orders the tiles' generic writes
 // before its products' reads (one proxy fence after each wait).  Tiles are
 // 128-byte-swizzled; eight lanes that store together take 4 tokens x 2 groups,
 // which the swizzle spreads over all banks.
+//
+// Measured over contexts of 104 and 110 K tokens, 4 heads, 224 rows each (44 tiles a
+// CTA): this kernel 121 us, 5.4 thousand cycles a tile, tensor pipes 38 % active,
+// issue slots 36 %; the weights' kernel 82 us, 3.6 thousand, 25 % and 37 %.  Neither
+// pipe is what they wait for: the roles wait for one another, a tile's widening,
+// products and softmax being one chain that the streams and the ring overlap in part.
 
 #include <math.h>
 #include <stdint.h>
@@ -61,7 +64,11 @@ static_assert(256 * (kLaunchRegs - kOtherRegs) >= 256 * (kSoftRegs - kLaunchRegs
 // The weights' kernel: eight warps add, four widen, one issues, one copies, six bring the queries.
 constexpr int kQueryWarps = 6;
 constexpr int kWeightThreads = (kSoftWarps + kWidenWarps + 2 + kQueryWarps) * 32;
-constexpr int kMinPiece = 8;   // tiles; shorter pieces cost more to join than they save
+// Tiles of the shortest piece (4, 16 in brackets), 224 rows a key/value head: one
+// request of 4 heads and up to 1600 tokens 33 us (29, 41), of up to 5000 40 (33, 50);
+// 2 requests of 32 heads and up to 1600 tokens 50 (49, 41); with more pieces than
+// CTAs either way no difference.
+constexpr int kMinPiece = 8;
 
 // ---------------------------------------------------------------------------
 // Plan: one CTA

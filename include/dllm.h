@@ -851,12 +851,16 @@ int dllm_kv4_write(const dllm_kv4_write_args* args, void* stream);
  * queries gave it:
  *   weights[page][g][slot] = prior[page][g][slot] + sum over the L positions
  *     and the q_heads / heads query heads of g of exp(a_j - lse)
- * (prior NULL: 0; prior may be weights; slots past lens[b] are not written;
- * no atomics, so equal calls give equal bits).  Pages shared between requests
+ * (prior NULL: 0; prior may be weights; slots past lens[b] are not written; no
+ * atomics).  Pages shared between requests
  * must not be given weights in one call.
  * Keys and values enter the products exactly; queries are scaled by a power
  * of two per row into fp16 range; softmax weights are rounded to fp16 for the
  * product with the values; sums and statistics are held in 32 bits.
+ * Equal calls give equal bits.  How a request's tokens are cut, and with it the
+ * last bits of out, lse and weights, depends on the batch: on the number of
+ * requests, heads and positions, on max_pages, and above 32 rows per key/value
+ * head (L * q_heads / heads) on the other requests' lengths.
  * lens[b] may be anything up to max_pages * page_size.
  * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_WORKSPACE,
  * DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
