@@ -9,8 +9,13 @@
 // score passes it by more than 15: 2^(a_j - m) stays below 2^15, inside fp16's
 // range, moves are rare, and weights down to 2^-31 of a row's largest keep
 // their place in fp16.  The weights are rounded to fp16 for the product with the
-// values; keys and values are exact in fp16 (see kv4.cuh), so a score's only
-// roundings are the tensor cores' 32-bit sums.
+// values, as the tensor cores take them: within 2^-11 of each, an eighth of what
+// rounding the output to bf16 costs it.  (Outputs are 0.0017 of their norm from 64
+// bits, as those of a 32-bit softmax rounded to bf16 are; the weights' other bits
+// would be a second product with the values.)  The normaliser l sums them before
+// that rounding.  Keys and values are exact in fp16 (see kv4.cuh), queries down to
+// 2^-16 of their row's largest (see kv4_mma.cuh), so a score's only other roundings
+// are the tensor cores' 32-bit sums.
 //
 // The weights of the tokens need every row's lse first, so a second kernel forms
 // the scores again and adds 2^(a_j - lse) over the rows, one warp owning a token.
