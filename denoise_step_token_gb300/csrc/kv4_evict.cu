@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const __grid_co
         }
         if (lost) set_error(P.C.err, DLLM_DEVERR_PAGE);
     }
+    for (int i = kKeys + tid; i < count; i += kSelThreads)   // the keys not held: their pages, once
+        if (token_page(P, b, j0 + i) < 0) set_error(P.C.err, DLLM_DEVERR_PAGE);
     __syncthreads();
     auto key_at = [&](int i) {
         return i < kKeys ? sh.keys[i] : weight_key(token_weight(P, token_page(P, b, j0 + i), head, j0 + i));

@@ -211,3 +211,26 @@ def test_attend_rows_at_the_rules_edges(dllm, L, H, D):
     lens = [0, 1, 128, 129, 400, 1300]
     cache = Cache(rng, lens, 1, D, 32)
     check_attend(dllm, cache, rng.standard_normal((len(lens), L, H, D)), weights=True)
+
+
+def test_evict_reports_pages_far_into_a_long_cache(dllm):
+    """A table entry outside the pool is recorded wherever its tokens lie, kept or
+    not; the other requests' choices stand."""
+    import torch
+    dev = torch.device("cuda", 0)
+    heads, page, n = 80, 256, 13 * 1024
+    per = n // page
+    pages, weights = dllm.kv4_pages(2 * per + 2, heads, page, 64, dev)
+    weights.copy_(1 + torch.rand(weights.shape, device=dev))
+    table = torch.arange(2 * per, dtype=torch.int32, device=dev).reshape(2, per)
+    dst = torch.tensor([[2 * per], [2 * per + 1]], dtype=torch.int32, device=dev)
+    lens, keep = (torch.full((2,), x, dtype=torch.int32, device=dev) for x in (n, 40))
+    good = dllm.kv4_evict(pages, weights.clone(), table, lens, keep, dst)
+    assert dllm.get_device_error(dev) == 0
+    for where in (0, 30, per - 2):
+        for entry in (-1, 2 * per + 2):
+            bad = table.clone()
+            bad[0, where] = entry
+            out = dllm.kv4_evict(pages, weights.clone(), bad, lens, keep, dst)
+            assert dllm.get_device_error(dev) == 5, (where, entry)
+            assert torch.equal(out["src"][1], good["src"][1])
