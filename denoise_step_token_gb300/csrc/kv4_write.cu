@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
     pdl_release();
     const int b = blockIdx.z;
     const int first = P.first ? P.first[b] : 0;
-    const int count = P.count ? P.count[b] : P.W - first;
+    const int count = P.count ? P.count[b] : P.W - max(first, 0);   // a negative first is refused below
     const int pos = P.pos[b];
     if (count <= 0) return;
     if (pos < 0 || (long long)pos + count > P.C.max_tokens || first < 0 || (long long)first + count > P.W) {

@@ -234,3 +234,21 @@ def test_evict_reports_pages_far_into_a_long_cache(dllm):
             out = dllm.kv4_evict(pages, weights.clone(), bad, lens, keep, dst)
             assert dllm.get_device_error(dev) == 5, (where, entry)
             assert torch.equal(out["src"][1], good["src"][1])
+
+
+@pytest.mark.parametrize("first", [-1, -5, -2 ** 31])
+def test_write_first_columns_below_zero(dllm, first):
+    """Recorded however far below, with the columns counted or not; nothing is
+    written for that request."""
+    import torch
+    dev = torch.device("cuda", 0)
+    pages, _ = dllm.kv4_pages(4, 1, 16, 64, dev)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device=dev)
+    k = torch.randn(2, 4, 1, 64, device=dev).to(torch.bfloat16)
+    pos = torch.zeros(2, dtype=torch.int32, device=dev)
+    start = torch.tensor([first, 1], dtype=torch.int32, device=dev)
+    for count in (None, torch.tensor([3, 3], dtype=torch.int32, device=dev)):
+        pages.zero_()
+        dllm.kv4_write(k, k, pages, table, pos, first=start, count=count)
+        assert dllm.get_device_error(dev) == 5
+        assert not pages[:2].any() and pages[2].any()
