@@ -857,6 +857,8 @@ int dllm_kv4_write(const dllm_kv4_write_args* args, void* stream);
  * Keys and values enter the products exactly; queries are scaled by a power
  * of two per row into fp16 range; softmax weights are rounded to fp16 for the
  * product with the values; sums and statistics are held in 32 bits.
+ * Scores a_j are taken to stay within 2^22 in magnitude: beyond about 2^12 their
+ * 32 bits show in out and weights, beyond 2^23 weights may pass fp16's range.
  * Equal calls give equal bits.  How a request's tokens are cut, and with it the
  * last bits of out, lse and weights, depends on the batch: on the number of
  * requests, heads and positions, on max_pages, and above 32 rows per key/value

@@ -204,9 +204,10 @@ def test_refused_shapes(dllm):
 
 # query rows per key/value head at the edges of the kernels' rules, with the tokens' weights
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("L,H", [(8, 4), (11, 3), (16, 7), (32, 4), (43, 3), (32, 8), (33, 8), (64, 8), (100, 7)])
+@pytest.mark.parametrize("L,H", [(8, 4), (11, 3), (16, 7), (32, 4), (43, 3), (32, 8), (33, 8), (64, 8), (257, 1), (100, 7)])
 def test_attend_rows_at_the_rules_edges(dllm, L, H, D):
-    """32, 33, 112, 128, 129, 256, 264, 512 and 700 rows."""
+    """32, 33, 112, 128, 129, 256, 264, 512, 257 and 700 rows: of 257, the second
+    block's rows leave a stream without any."""
     rng = np.random.default_rng(42)
     lens = [0, 1, 128, 129, 400, 1300]
     cache = Cache(rng, lens, 1, D, 32)
