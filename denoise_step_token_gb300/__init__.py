@@ -19,6 +19,7 @@ Names follow the C ABI in ``include/dllm.h``:
 * ``kv4_pages`` / ``kv4_write`` / ``kv4_attend`` / ``kv4_evict`` -- the paged
   cache of keys and values in 4 bits: its pool, the write, a block's
   attention over it, and its thinning by attention weight.
+* ``sample`` -- tokens drawn from the step's logits by given random numbers.
 """
 from __future__ import annotations
 
@@ -32,7 +33,7 @@ import numpy as np
 from . import _build
 
 __all__ = ["load", "step", "step_host", "features", "pack_plan", "admit", "pack", "advance", "compact", "refill",
-           "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict",
+           "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict", "sample",
            "get_device_error", "DllmError", "NUM_FEATURES", "LIB_PATH"]
 
 LIB_PATH = _build.LIB_PATH
@@ -141,6 +142,11 @@ class Kv4EvictArgs(ctypes.Structure):
                 ("weights", _p), ("dst_table", _p), ("dst_lens", _p), ("src", _p)]
 
 
+class SampleArgs(ctypes.Structure):
+    _fields_ = [("N", _i32), ("V", _i32), ("ldv", _i64), ("logits_rows", _i64), ("logits", _p), ("rows", _p), ("u", _p),
+                ("temperature", _p), ("top_k", _p), ("top_p", _p), ("min_p", _p), ("tokens", _p), ("prob", _p)]
+
+
 MAX_TOP = 32
 KV4_GROUP = 32
 
@@ -205,6 +211,7 @@ _SIGNATURES = {
     "dllm_kv4_attend_workspace_size": (_sz, [ctypes.POINTER(Kv4Cache), _i32, _i32]),
     "dllm_kv4_attend": (ctypes.c_int, [ctypes.POINTER(Kv4AttendArgs), _p]),
     "dllm_kv4_evict": (ctypes.c_int, [ctypes.POINTER(Kv4EvictArgs), _p]),
+    "dllm_sample": (ctypes.c_int, [ctypes.POINTER(SampleArgs), _p]),
 }
 
 
@@ -242,7 +249,7 @@ def load(build=True):
             raise RuntimeError(f"libdllm ABI version {lib.dllm_abi_version()}, binding expects {ABI_VERSION}")
         for which, cls in enumerate((StepArgs, PackArgs, CompactArgs, AdvanceArgs, RefillArgs, LoopConfig, LoopInfo,
                                      VocabShard, LoopControl, LogprobsArgs, Kv4Cache, Kv4WriteArgs, Kv4AttendArgs,
-                                     Kv4EvictArgs)):
+                                     Kv4EvictArgs, SampleArgs)):
             if lib.dllm_struct_size(which) != ctypes.sizeof(cls):
                 raise RuntimeError(f"ABI mismatch for {cls.__name__}: library {lib.dllm_struct_size(which)} "
                                    f"bytes, binding {ctypes.sizeof(cls)}")
@@ -992,3 +999,45 @@ def kv4_evict(pages, weights, table, lens, keep, dst_table, *, recent=0):
     if rc:
         _check("dllm_kv4_evict", rc)
     return {"lens": new_lens, "src": src}
+
+
+# ---------------------------------------------------------------------------
+# draws
+# ---------------------------------------------------------------------------
+def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=None, min_p=None):
+    """Draw one token for each row of logits by given random numbers
+    (dllm_sample) on the current stream.
+
+    logits:      bf16 CUDA tensor of rows (last dimension the row stride,
+                 16-byte rows), V (default: the stride) values each
+    u:           float32 [N] random numbers in [0, 1)
+    rows:        int32 [N] row of each entry (-1: skip), or None: entry i is
+                 row i
+    temperature: float32 [N] (0: the most likely token), default 1
+    top_k:       int32 [N] (0: all); top_p, min_p: float32 [N] (1 and 0: all)
+    Returns a dict: tokens (int32 [N], -1 for skipped and invalid rows) and
+    prob (float32 [N]), the probability with which each was drawn."""
+    torch = _torch()
+    dev = logits.device
+    _check_tensors(torch, dev, logits, u, rows, temperature, top_k, top_p, min_p)
+    float32, int32 = torch.float32, torch.int32
+    if logits.dtype != torch.bfloat16:
+        raise TypeError("logits must be bf16")
+    N = u.numel()
+    for name, t, dtype in (("u", u, float32), ("rows", rows, int32), ("temperature", temperature, float32),
+                           ("top_k", top_k, int32), ("top_p", top_p, float32), ("min_p", min_p, float32)):
+        if t is not None and (t.dtype != dtype or t.numel() != N):
+            raise TypeError(f"{name} must be {dtype} [{N}]")
+    ldv = logits.shape[-1]
+    n_rows = logits.numel() // ldv if ldv else 0
+    if rows is None and n_rows < N:
+        raise ValueError("one row per random number")
+    out = {"tokens": torch.empty(N, dtype=int32, device=dev), "prob": torch.empty(N, dtype=float32, device=dev)}
+    a = SampleArgs(N, ldv if V is None else V, ldv, n_rows, logits.data_ptr(), None if rows is None else rows.data_ptr(),
+                   u.data_ptr(), None if temperature is None else temperature.data_ptr(),
+                   None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+                   None if min_p is None else min_p.data_ptr(), out["tokens"].data_ptr(), out["prob"].data_ptr())
+    rc = (_lib or load()).dllm_sample(ctypes.byref(a), _raw_stream(torch, dev))
+    if rc:
+        _check("dllm_sample", rc)
+    return out

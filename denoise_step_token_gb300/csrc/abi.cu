@@ -109,6 +109,7 @@ extern "C" size_t dllm_struct_size(int which) {
         case 11: return sizeof(dllm_kv4_write_args);
         case 12: return sizeof(dllm_kv4_attend_args);
         case 13: return sizeof(dllm_kv4_evict_args);
+        case 14: return sizeof(dllm_sample_args);
         default: return 0;
     }
 }

@@ -78,8 +78,8 @@ int dllm_last_cuda_error(const char** name);
  * 3 dllm_advance_args, 4 dllm_refill_args, 5 dllm_loop_config,
  * 6 dllm_loop_info_t, 7 dllm_vocab_shard, 8 dllm_loop_control,
  * 9 dllm_logprobs_args, 10 dllm_kv4_cache, 11 dllm_kv4_write_args,
- * 12 dllm_kv4_attend_args, 13 dllm_kv4_evict_args.  Returns 0 for an unknown
- * `which`. */
+ * 12 dllm_kv4_attend_args, 13 dllm_kv4_evict_args, 14 dllm_sample_args.
+ * Returns 0 for an unknown `which`. */
 size_t dllm_struct_size(int which);
 
 /* Fault injection for tests of the status plumbing (host only; nothing
@@ -915,6 +915,49 @@ typedef struct dllm_kv4_evict_args {
 } dllm_kv4_evict_args;
 
 int dllm_kv4_evict(const dllm_kv4_evict_args* args, void* stream);
+
+/* ======================================================================
+ * Draws.  One token for each of N logits rows, by given random numbers: the
+ * sampled counterpart of the step's argmax (S2); with dllm_step_merge (one
+ * "shard", m = 0, s = 1 / prob, idx = tokens) the step commits drawn tokens.
+ *
+ * Entry i, over x = the V values of logits row r (r = rows[i], or i when rows
+ * is NULL), T = temperature[i], in the order of falling values (ties: lowest
+ * token first; -0 == +0), with w_v = exp((x_v - max x) / T):
+ *   1. kept: the first top_k[i] tokens (top_k <= 0: all), of them those with
+ *      w_v >= min_p[i] (min_p <= 0 or NaN: all);
+ *   2. with top_p[i] < 1, of these the shortest prefix whose mass (sum of w)
+ *      is >= top_p[i] times the mass of all of them (at least one token);
+ *   3. the token: the first whose cumulative mass is > u[i] times the kept
+ *      mass (u >= 1: the last kept one; u < 0 or NaN: the first).
+ *   tokens[i] = that token, prob[i] = its w over the kept mass.
+ * T == 0 takes the first token of the order, with prob 1.  T < 0 or NaN, a row
+ * without a finite maximum (all -inf, or holding +inf or NaN) and a row number
+ * outside [0, logits_rows) (-1: skip) give -1 and NaN.  NULL temperature is 1,
+ * NULL top_k, top_p, min_p keep everything.
+ * Cumulative masses are held to about 2^-40 of the whole (64-bit fixed point
+ * over the counts of a row's different values), whatever V: the draw is the
+ * definition's but where u lies that close to a border.  Tokens with weights
+ * below 2^-75 of the largest are not drawn.  A row's result depends on that row
+ * alone.  Serves sampling: no gradient. */
+typedef struct dllm_sample_args {
+    int32_t N;                  /* entries (>= 0) */
+    int32_t V;                  /* vocabulary size, 1..2^28 */
+    int64_t ldv;                /* row stride in elements: >= V, a multiple of 8 */
+    int64_t logits_rows;        /* rows of logits (>= 0) */
+    const uint16_t* logits;     /* device bf16 [logits_rows][ldv], 16-byte aligned */
+    const int32_t* rows;        /* device [N] row of each entry, or NULL */
+    const float* u;             /* device [N] in [0, 1) */
+    const float* temperature;   /* device [N], or NULL: 1 */
+    const int32_t* top_k;       /* device [N], or NULL */
+    const float* top_p;         /* device [N], or NULL */
+    const float* min_p;         /* device [N], or NULL */
+    int32_t* tokens;            /* device [N] out */
+    float* prob;                /* device [N] out */
+} dllm_sample_args;
+
+/* Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+int dllm_sample(const dllm_sample_args* args, void* stream);
 
 #ifdef __cplusplus
 }
