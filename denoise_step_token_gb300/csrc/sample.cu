@@ -14,7 +14,7 @@
 // of the tokens with that value, counted from the lowest, it is.
 //
 // Split.  A cluster of 1 to 8 CTAs takes a row, each CTA a slice: a copying warp
-// keeps the ring of bulk copies full (also with the next rows' pieces), eight
+// keeps the ring of bulk copies full (also with the next rows' pieces), sixteen
 // warps count values with shared-memory atomics.  Segments of 32 values are
 // summed by all warps of the cluster (counts of the others by distributed shared
 // memory), one warp walks the segments' sums, and the CTA whose slice holds the
@@ -31,7 +31,7 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;   // counting threads of a CTA
+constexpr int kThreads = 512;   // counting threads of a CTA (256: 320 us instead of 292, 1851 rows of 151936)
 constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 7;
 constexpr int kChunk = 4096;    // values of a stage
@@ -50,13 +50,11 @@ constexpr int kSegments = 2 * kHalfBins / 32;
 constexpr int kWindow = 4096;
 constexpr int kWideSegment = 64;
 constexpr int kWideSegments = 65536 / kWideSegment;
-constexpr int kList = 1024;     // tokens of the drawn value held at once
-constexpr int kBuckets = 256;
 
-// Tables of 2^(i / 16^(l+1)): level 0 in units of 2^-62, the others less 1 in
-// units of 2^-64, from square roots of 2 in whole numbers.
+// 2^(i / 256) in units of 2^-63, i in [0, 256), from square roots of 2 in whole numbers.
+constexpr int kPowers = 256;
 struct PowerTable {
-    u64 t[4][16];
+    u64 t[kPowers];
 };
 constexpr u64 root_of(unsigned __int128 v) {   // floor of the square root
     u64 r = 0;
@@ -67,24 +65,23 @@ constexpr u64 root_of(unsigned __int128 v) {   // floor of the square root
     return r;
 }
 constexpr PowerTable make_powers() {
-    u64 root[16] = {};                         // 2^(2^-(k+1)) in units of 2^-63
-    unsigned __int128 v = (unsigned __int128)1 << 127;   // 2 * 2^126
-    for (int k = 0; k < 16; ++k) {
+    u64 root[8] = {};                                    // 2^(2^-(k+1))
+    unsigned __int128 v = (unsigned __int128)1 << 127;   // 2, in units of 2^-126
+    for (int k = 0; k < 8; ++k) {
         root[k] = root_of(v);
         v = (unsigned __int128)root[k] << 63;
     }
     PowerTable p = {};
-    for (int l = 0; l < 4; ++l)
-        for (int i = 0; i < 16; ++i) {
-            unsigned __int128 x = (unsigned __int128)1 << 63;
-            for (int b = 0; b < 4; ++b)
-                if (i >> b & 1) x = x * root[4 * l + 3 - b] >> 63;
-            p.t[l][i] = l == 0 ? (u64)(x >> 1) : (u64)((x - ((unsigned __int128)1 << 63)) << 1);
-        }
+    for (int i = 0; i < kPowers; ++i) {
+        unsigned __int128 x = (unsigned __int128)1 << 63;
+        for (int b = 0; b < 8; ++b)
+            if (i >> b & 1) x = x * root[7 - b] >> 63;
+        p.t[i] = (u64)x;
+    }
     return p;
 }
 __constant__ PowerTable c_powers = make_powers();
-static_assert(make_powers().t[0][8] == 6521908912666391106ull, "sqrt(2) * 2^62");
+static_assert(make_powers().t[128] == 13043817825332782212ull, "sqrt(2) * 2^63");
 
 struct SampleParams {
     int N, V;
@@ -103,6 +100,60 @@ struct SampleParams {
     int shift;            // masses are in units of 2^(shift - 62)
 };
 
+// The weights of one row's values, by pairs of 32-bit floats and whole numbers (64-bit floating point runs at 2 operations
+// an SM and cycle here).
+struct Weights {
+    float m;           // the maximum
+    float scale;       // 1, or 2^-64 for temperatures where log2(e) / T would lose bits
+    float s, s_low;    // log2(e) / T in two parts, over `scale`
+    u64 least;         // min-p in units of 2^-62: smaller weights are left out
+    int shift;
+
+    __device__ __forceinline__ void set(float top, float T, float min_p) {
+        m = top;
+        T = fmaxf(T, 1.17549435e-38f);
+        scale = T > 1.8446744e19f ? 5.4210109e-20f : 1.0f;
+        const float t = T * scale;   // inf stays
+        constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
+        s = kLog2e / t;
+        s_low = isinf(t) ? 0.0f : (fmaf(-s, t, kLog2e) + kLog2eLow) / t;
+        least = min_p > 0.0f ? __float2ull_ru(fminf(min_p, 1.0f) * 4.611686e18f) : 0;
+    }
+    // (x - m) s to 32 bits.
+    __device__ __forceinline__ float rough(float x) const { return (x * scale - m * scale) * s; }
+    // w in units of 2^-62; 0 below that and where min-p leaves the value out.  No branches: callers have several under way.
+    __device__ __forceinline__ u64 of(float x, const u64* powers) const {
+        // x - m = d + e without error, its product with s = p + rest
+        const float xs = x * scale, ms = -m * scale;
+        const float d = xs + ms, v = d - xs, e = (xs - (d - v)) + (ms - v);
+        const float p = d * s;
+        const bool live = p > -62.0f;   // p <= 0
+        const float rest = fmaf(e, s, fmaf(d, s_low, fmaf(d, s, -p)));
+        // p = j / 256 + h, |h| <= 2^-9
+        const float at = fmaf(fmaxf(p, -64.0f), 256.0f, 12582912.0f);
+        const int j = __float_as_int(at) - 0x4b400000;
+        const float h = fmaf(at - 12582912.0f, -0.00390625f, fmaxf(p, -64.0f));
+        // 2^(h + rest) - 1: the leading product h ln 2 in two parts, the other powers behind it
+        constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;
+        const float g = h * kLn2;
+        float more = fmaf(h, 9.61812911e-3f, 5.55041087e-2f);
+        more = fmaf(h, more, 2.40226507e-1f);
+        more = fmaf(h * h, more, fmaf(rest, kLn2, fmaf(h, kLn2Low, fmaf(h, kLn2, -g))));
+        // in units of 2^-40: g to 31 bits, the rest by its place behind 1.5 * 2^23
+        const int part = __float2int_rn(g * 1.09951163e12f) + (__float_as_int(fmaf(more, 1.09951163e12f, 12582912.0f)) - 0x4b400000);
+        const u64 t = powers[j & 255];
+        // t (1 + part 2^-40), the product with t's upper 32 bits
+        const long long add = ((long long)part << 31) + (long long)part * (int)((t >> 32) - 0x80000000u);
+        const u64 w = (u64)((long long)(t >> 1) + (add >> 9)) >> (-(j >> 8) & 63);
+        return live && w >= least ? w : 0;
+    }
+    // Mass of `count` tokens of weight w.
+    __device__ __forceinline__ u64 mass(uint32_t count, u64 w) const {
+        const u64 lo = (u64)count * (uint32_t)w, hi = (u64)count * (uint32_t)(w >> 32);
+        return (hi << (32 - shift)) + ((lo + (1ull << (shift - 1))) >> shift);
+    }
+};
+
 // What a CTA tells the others of its slice.
 struct SliceFacts {
     float max;    // NaN if the slice holds one
@@ -110,24 +161,35 @@ struct SliceFacts {
     int low;      // values at or under -2^8
 };
 
-struct Draw {
-    uint32_t bits;  // the value; zero stands for both zeros
-    long long r;    // which of its tokens
-    float prob;
+struct Found {
+    u64 mass;        // of the tokens up to and with the one found
+    uint32_t bits;   // its value; 0 stands for both zeros
+    uint32_t r, n;   // which of the value's n tokens, from 0
+    u64 w;
+};
+
+// What the functions behind the counting need of the row, in shared memory: they run once a row, and parameters behind
+// a pointer or on the stack are fetched from L2 each time (sums of a row: 32,000 cycles so).
+struct RowFacts {
+    Weights W;
+    const uint16_t* x;
+    int V, cluster;
 };
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], meet[2];
-    u64 powers[4][16];
+    u64 powers[kPowers];
     u64 seg_mass[kSegments];
     uint32_t seg_count[kSegments];
-    int list[kList];
-    int buckets[kBuckets];
+    u64 warp_mass[kWarps];
+    uint32_t warp_count[kWarps];
+    uint32_t groups[64], counts[3];
     float part[kWarps];
     SliceFacts facts;
-    Draw draw;
-    u64 found_mass;
-    int abort, count, segment, flag;
+    Found found;
+    u64 kept;
+    RowFacts row;
+    int abort, segment, flag;
 };
 constexpr uint32_t kGap = (kValues + 1) * 4 + 15 & ~15u;   // the struct lies between the counters of both signs
 static_assert(kGap + sizeof(Shared) <= kNegative, "fits between the counters");
@@ -137,7 +199,7 @@ static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 // the wide path's: window counters where the negatives' are, segment sums where the positives' are
 static_assert(kWindow * 4 <= (kValues + 1) * 4 && kWideSegments * 12 <= kGap, "the wide path's arrays");
 
-__device__ __forceinline__ void sync_warps() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void sync_warps() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 // All threads of the cluster, before their roles part.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -152,11 +214,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t at, int cta) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(at), "r"(cta));
     return p;
 }
-__device__ __forceinline__ uint32_t peer_load(uint32_t at, int cta) {
+__device__ __forceinline__ uint32_t cluster_load(uint32_t at) {
     uint32_t v;
-    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(peer_addr(at, cta)) : "memory");
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at));
     return v;
 }
+__device__ __forceinline__ uint32_t peer_load(uint32_t at, int cta) { return cluster_load(peer_addr(at, cta)); }
 __device__ __forceinline__ void peer_store(uint32_t at, int cta, uint32_t v) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(at, cta)), "r"(v) : "memory");
 }
@@ -189,7 +252,7 @@ struct Meeting {
                              peer_addr(bars + (n & 1) * 8, threadIdx.x))
                          : "memory");
     }
-    __device__ __forceinline__ void wait(int* abort, int* err) {
+    __device__ __noinline__ void wait(int* abort, int* err) {
         const uint32_t bar = bars + (n & 1) * 8, parity = n >> 1 & 1;
         ++n;
         if (*(volatile int*)abort || meet_try(bar, parity)) return;
@@ -222,42 +285,6 @@ __device__ __forceinline__ void count_at(uint32_t addr) {
     asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(addr));
 }
 
-// The weights of one row's values.
-struct Weights {
-    double m, s;      // the maximum; log2(e) / T
-    float m32, s32;
-    u64 least;        // min-p in units of 2^-62: smaller weights are left out
-    int shift;
-
-    // w in units of 2^-62; 0 below 2^-75 and where min-p leaves the value out.
-    __device__ __forceinline__ u64 of(float x, const u64 (*pw)[16]) const {
-        if (x == m32) return 1ull << 62;
-        if (!((x - m32) * s32 > -75.0f)) return 0;
-        // y = (x - m) s, rounded to 2^-44: 384 + y stays in [256, 512)
-        const double r = fma((double)x - m, s, 384.0);
-        const long long y = __double_as_longlong(r) - __double_as_longlong(384.0);
-        const int n = (int)(y >> 44);                       // <= -1, or 0 with no fraction
-        const uint32_t hi = (uint32_t)(y >> 28);            // the 16 upper bits of the fraction
-        const u64 rest = (u64)(y & 0xfffffffll);            // < 2^-16
-        // 2^rest - 1 = a + a^2 / 2, a = rest ln 2 (what follows is under 2^-51), in units of 2^-64
-        const u64 a = rest * 0xb17217f8ull >> 12;
-        const u64 a24 = a >> 24;
-        u64 w = pw[0][hi >> 12 & 15];
-        w += __umul64hi(w, pw[1][hi >> 8 & 15]);
-        w += __umul64hi(w, pw[2][hi >> 4 & 15]);
-        w += __umul64hi(w, pw[3][hi & 15]);
-        w += __umul64hi(w, a + (a24 * a24 >> 17));
-        w >>= min(-n, 63);
-        return w >= least ? w : 0;
-    }
-    __device__ __forceinline__ double unit() const { return __longlong_as_double((long long)(1023 - shift) << 52); }
-    // Mass of `count` tokens of weight w.
-    __device__ __forceinline__ u64 mass(uint32_t count, u64 w) const {
-        const u64 lo = (u64)count * (uint32_t)w, hi = (u64)count * (uint32_t)(w >> 32);
-        return (hi << (32 - shift)) + ((lo + (1ull << (shift - 1))) >> shift);
-    }
-};
-
 __device__ __forceinline__ u64 warp_sum64(u64 v) {   // v < 2^59
     const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7ffffffu);
     const uint32_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27) & 0x7ffffffu);
@@ -265,20 +292,19 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {   // v < 2^59
     return (u64)lo + ((u64)mid << 27) + ((u64)hi << 54);
 }
 
-// One row as a cluster (rank 0 to `cluster` - 1) or, in the wide path, rank 0 alone
-// sees it.
-struct Row {
-    const SampleParams& P;
-    Shared& sh;
-    unsigned char* smem;
-    uint32_t base;           // of the dynamic shared memory
-    const uint16_t* x;
-    Weights W;
-    bool wide;
+extern __shared__ __align__(128) unsigned char smem[];
 
-    // The value of bin o, in falling order.
-    __device__ __forceinline__ uint32_t bits_of(int o) const {
-        if (wide) {
+__device__ __forceinline__ Shared& shared() { return *reinterpret_cast<Shared*>(smem + kGap); }
+__device__ __forceinline__ uint32_t word_at(uint32_t at) { return *reinterpret_cast<const uint32_t*>(smem + at); }
+
+// The bins of a row, in falling order of their values: kSegments * 32 of the counters, or (kWide) all keys.
+template <bool kWide>
+struct Bins {
+    static constexpr int kCount = kWide ? kWideSegments : kSegments;   // of segments
+    static constexpr int kSize = kWide ? kWideSegment : 32;            // of one
+
+    static __device__ __forceinline__ uint32_t bits(int o) {
+        if (kWide) {
             const uint32_t key = 0xffffu - o;
             return key & 0x8000u ? key ^ 0x8000u : ~key & 0xffffu;
         }
@@ -288,311 +314,365 @@ struct Row {
         }
         return 0x8000u | (kLow + (o - kHalfBins));
     }
-    // Its counters, over the cluster.  Bins without a value of their own: 0.
-    __device__ __forceinline__ uint32_t count_of(int o) const {
-        if (wide) return reinterpret_cast<const uint32_t*>(smem + kNegative)[o];
-        const bool neg = o >= kHalfBins;
-        const int c = neg ? o - kHalfBins : kHalfBins - 1 - o;
-        if (c >= kValues || (neg && c == 0)) return 0;
-        const uint32_t at = (neg ? kNegative : 0u) + c * 4;
-        uint32_t n = 0;
-        if (P.cluster == 1) {
-            n = *reinterpret_cast<const uint32_t*>(smem + at);
-            if (c == 0) n += *reinterpret_cast<const uint32_t*>(smem + kNegative);   // -0 is 0
-            return n;
-        }
-#pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-            if (q < P.cluster) {
-                n += peer_load(base + at, q);
-                if (c == 0) n += peer_load(base + kNegative, q);
-            }
-        return n;
+    static __device__ __forceinline__ float value(int o) { return __uint_as_float(bits(o) << 16); }
+    static __device__ __forceinline__ uint32_t* seg_count() {
+        return kWide ? reinterpret_cast<uint32_t*>(smem + kWideSegments * 8) : shared().seg_count;
     }
-    __device__ __forceinline__ int segments() const { return wide ? kWideSegments : kSegments; }
-    __device__ __forceinline__ int segment_bins() const { return wide ? kWideSegment : 32; }
-    __device__ __forceinline__ uint32_t seg_count(int s) const {
-        return wide ? reinterpret_cast<const uint32_t*>(smem + kWideSegments * 8)[s] : sh.seg_count[s];
-    }
-    __device__ __forceinline__ u64 seg_mass(int s) const {
-        return wide ? reinterpret_cast<const u64*>(smem)[s] : sh.seg_mass[s];
-    }
+    static __device__ __forceinline__ u64* seg_mass() { return kWide ? reinterpret_cast<u64*>(smem) : shared().seg_mass; }
+};
 
-    // Counts the row's values with keys 0xffff - o for o in [o0, o0 + n), n a power of two (wide path; every thread).
-    __device__ void count_keys(int o0, int n) const {
-        uint32_t* const counts = reinterpret_cast<uint32_t*>(smem + kNegative);
-        for (int i = threadIdx.x; i < n; i += kThreads) counts[i] = 0;
+// The counts of kN bins, over the cluster.
+template <int kN>
+__device__ __forceinline__ void counts_of(const int (&o)[kN], uint32_t (&n)[kN], int cluster) {
+    uint32_t at[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        const bool neg = o[j] >= kHalfBins;
+        const int c = neg ? o[j] - kHalfBins : kHalfBins - 1 - o[j];
+        at[j] = (neg ? kNegative : 0u) + min(c, kValues) * 4;
+        n[j] = word_at(at[j]);
+    }
+    if (cluster > 1) {
+        const uint32_t base = smem_addr(smem);
+        const int self = (int)cluster_rank();
+#pragma unroll 1
+        for (int q = 1; q < cluster; ++q) {   // its size is a power of two
+            const uint32_t from = peer_addr(base, self ^ q);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) n[j] += cluster_load(from + at[j]);
+        }
+    }
+    // bins without a value of their own took the last counter, which is left out
+#pragma unroll
+    for (int j = 0; j < kN; ++j) n[j] = (at[j] & ~kNegative) == kValues * 4 ? 0 : n[j];
+}
+
+// The segments' sums become sums up to and with each segment (every thread).
+template <bool kWide>
+__device__ __noinline__ void add_up() {
+    Shared& sh = shared();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int n = Bins<kWide>::kCount, per = (n + kThreads - 1) / kThreads;
+    uint32_t* const counts = Bins<kWide>::seg_count();
+    u64* const masses = Bins<kWide>::seg_mass();
+    uint32_t cs[per], c = 0;
+    u64 ms[per], m = 0;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        c += cs[k] = s < n ? counts[s] : 0;
+        m += ms[k] = s < n ? masses[s] : 0;
+    }
+    const uint32_t c1 = c;
+    const u64 m1 = m;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t cy = __shfl_up_sync(0xffffffffu, c, off);
+        const u64 my = __shfl_up_sync(0xffffffffu, m, off);
+        if (lane >= off) {
+            c += cy;
+            m += my;
+        }
+    }
+    if (lane == 31) {
+        sh.warp_count[warp] = c;
+        sh.warp_mass[warp] = m;
+    }
+    sync_warps();
+    c -= c1;
+    m -= m1;
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w) {
+        c += w < warp ? sh.warp_count[w] : 0;
+        m += w < warp ? sh.warp_mass[w] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        c += cs[k];
+        m += ms[k];
+        if (s < n) {
+            counts[s] = c;
+            masses[s] = m;
+        }
+    }
+    sync_warps();
+}
+
+// Counts the row's values with keys 0xffff - o for o in [o0, o0 + n) (wide path; every thread).
+__device__ __noinline__ void count_keys(int o0, int n) {
+    uint32_t* const counts = reinterpret_cast<uint32_t*>(smem + kNegative);
+    const uint16_t* const x = shared().row.x;
+    const int V = shared().row.V;
+    for (int i = threadIdx.x; i < n; i += kThreads) counts[i] = 0;
+    sync_warps();
+#pragma unroll 1
+    for (int e = threadIdx.x * 8; e < V; e += kThreads * 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(x + e);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xffffu;
+            if (b == 0x8000u) b = 0;
+            const uint32_t o = 0xffffu - (b & 0x8000u ? ~b & 0xffffu : b | 0x8000u);
+            if (o - o0 < (uint32_t)n && b != 0xff80u && e + k < V) atomicAdd(&counts[o - o0], 1u);
+        }
+    }
+    sync_warps();
+}
+
+// The first token whose count reaches `target` (by_count), or whose cumulative mass does; a target within the totals.
+// The first warp calls; in the wide path every thread.  The answer is in shared memory.
+template <bool kWide>
+__device__ __noinline__ void find(bool by_count, u64 target) {
+    using B = Bins<kWide>;
+    Shared& sh = shared();
+    const int lane = threadIdx.x & 31;
+    uint32_t c0 = 0;
+    u64 m0 = 0;
+    int seg = 0;
+    if (threadIdx.x < 32) {
+        // the first segment that reaches the target: among every per-th one, then among the per before it
+        constexpr int last = B::kCount - 1, per = (B::kCount + 31) / 32;
+        auto reaches = [&](int s) { return (by_count ? (u64)B::seg_count()[s] : B::seg_mass()[s]) >= target; };
+        unsigned who = __ballot_sync(0xffffffffu, reaches(min(lane * per + per - 1, last)));
+        const int run = who ? (__ffs(who) - 1) * per : last;
+        who = __ballot_sync(0xffffffffu, reaches(min(run + min(lane, per - 1), last)));
+        seg = who ? min(run + __ffs(who) - 1, last) : last;
+        if (seg > 0) {
+            c0 = B::seg_count()[seg - 1];
+            m0 = B::seg_mass()[seg - 1];
+        }
+        if (kWide && lane == 0) sh.segment = seg;
+    }
+    if (kWide) {
         sync_warps();
-        for (int e = threadIdx.x * 8; e < P.V; e += kThreads * 8) {
-            const uint4 q = *reinterpret_cast<const uint4*>(x + e);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xffffu;
-                if (b == 0x8000u) b = 0;
-                const uint32_t o = 0xffffu - (b & 0x8000u ? ~b & 0xffffu : b | 0x8000u);
-                if (o - o0 < (uint32_t)n && b != 0xff80u && e + k < P.V) atomicAdd(&counts[o - o0], 1u);
-            }
-        }
-        sync_warps();
+        count_keys(sh.segment * B::kSize, B::kSize);
     }
-
-    struct Lane {      // sums before this lane's segments, and of them
-        uint32_t count0;
-        u64 mass0;
-        uint32_t total_count;
-        u64 total_mass;
-        int s0, s1;
-    };
-    // One warp: every lane's run of segments.
-    __device__ Lane walk() const {
-        const int lane = threadIdx.x & 31, n = segments(), per = (n + 31) / 32;
-        Lane L;
-        L.s0 = min(lane * per, n);
-        L.s1 = min(L.s0 + per, n);
-        uint32_t c = 0;
-        u64 m = 0;
-        for (int s = L.s0; s < L.s1; ++s) {
-            c += seg_count(s);
-            m += seg_mass(s);
-        }
-        uint32_t ci = c;
-        u64 mi = m;
+    if (threadIdx.x < 32) {
+        const Weights W = sh.row.W;
+#pragma unroll 1
+        for (int b0 = 0; b0 < B::kSize; b0 += 32) {
+            const int o[1] = {seg * B::kSize + b0 + lane};
+            uint32_t count[1];
+            if (kWide) count[0] = word_at(kNegative + (b0 + lane) * 4);
+            else counts_of(o, count, sh.row.cluster);
+            uint32_t n = count[0];
+            const u64 w = W.of(B::value(o[0]), sh.powers);
+            if (w == 0) n = 0;
+            uint32_t ci = n;
+            const u64 mine = W.mass(n, w);
+            u64 mi = mine;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t cy = __shfl_up_sync(0xffffffffu, ci, off);
-            const u64 my = __shfl_up_sync(0xffffffffu, mi, off);
-            if (lane >= off) {
-                ci += cy;
-                mi += my;
-            }
-        }
-        L.count0 = ci - c;
-        L.mass0 = mi - m;
-        L.total_count = __shfl_sync(0xffffffffu, ci, 31);
-        L.total_mass = __shfl_sync(0xffffffffu, mi, 31);
-        return L;
-    }
-
-    struct Found {
-        u64 mass;        // of the tokens up to and with the one found
-        uint32_t bits;   // its value
-        uint32_t r;      // which of the value's tokens, from 0
-        u64 w;
-    };
-    // The first token whose count reaches `target` (by_count), or whose cumulative mass does; a target within the
-    // totals.  The warp that walks calls with its lanes' sums; in the wide path every thread calls.
-    __device__ Found find(const Lane& L, bool by_count, u64 target) const {
-        const int lane = threadIdx.x & 31;
-        Found f = {};
-        uint32_t c0 = 0;
-        u64 m0 = 0;
-        int seg = 0;
-        if (threadIdx.x < 32) {
-            // the lane whose run holds the target, then its segment
-            uint32_t c = L.count0;
-            u64 m = L.mass0;
-            int mine = -1;
-            for (int s = L.s0; s < L.s1 && mine < 0; ++s) {
-                const uint32_t cn = c + seg_count(s);
-                const u64 mn = m + seg_mass(s);
-                if ((by_count ? (u64)cn : mn) >= target) {
-                    mine = s;
-                } else {
-                    c = cn;
-                    m = mn;
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t cy = __shfl_up_sync(0xffffffffu, ci, off);
+                const u64 my = __shfl_up_sync(0xffffffffu, mi, off);
+                if (lane >= off) {
+                    ci += cy;
+                    mi += my;
                 }
             }
-            const unsigned who = __ballot_sync(0xffffffffu, mine >= 0);
-            const int src = who ? __ffs(who) - 1 : 31;
-            seg = max(0, __shfl_sync(0xffffffffu, mine, src));
-            c0 = __shfl_sync(0xffffffffu, c, src);
-            m0 = __shfl_sync(0xffffffffu, m, src);
-            if (wide && lane == 0) sh.segment = seg;
-        }
-        if (wide) {
-            sync_warps();
-            count_keys(sh.segment * kWideSegment, kWideSegment);
-        }
-        if (threadIdx.x < 32) {
-            for (int b0 = 0; b0 < segment_bins(); b0 += 32) {
-                const int o = seg * segment_bins() + b0 + lane;
-                uint32_t n = count_of(wide ? b0 + lane : o);
-                const uint32_t bits = bits_of(o);
-                const u64 w = n ? W.of(__uint_as_float(bits << 16), sh.powers) : 0;
-                if (w == 0) n = 0;
-                uint32_t ci = n;
-                const u64 mine = W.mass(n, w);
-                u64 mi = mine;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const uint32_t cy = __shfl_up_sync(0xffffffffu, ci, off);
-                    const u64 my = __shfl_up_sync(0xffffffffu, mi, off);
-                    if (lane >= off) {
-                        ci += cy;
-                        mi += my;
-                    }
-                }
-                const u64 have = by_count ? (u64)(c0 + ci) : m0 + mi;
-                const unsigned who = __ballot_sync(0xffffffffu, n && have >= target);
-                if (who) {
+            const unsigned who = __ballot_sync(0xffffffffu, n && (by_count ? (u64)(c0 + ci) : m0 + mi) >= target);
+            if (who) {
+                if (lane == __ffs(who) - 1) {
                     // tokens of the bin that are needed, 1 to n
                     uint32_t j;
                     const u64 before = m0 + mi - mine;
                     if (by_count) {
                         j = (uint32_t)(target - (c0 + ci - n));
                     } else {
+                        // a quotient in 32 bits, twice made good, then to the token
                         const u64 rem = target > before ? target - before : 1;
-                        const double one = (double)w * W.unit();
-                        j = (uint32_t)min(max(ceil(((double)rem - 0.5) / one), 1.0), (double)n);
+                        const float ones = __frcp_rn((float)w * __uint_as_float((uint32_t)(127 - W.shift) << 23));
+                        j = (uint32_t)fminf(fmaxf((float)rem * ones, 1.0f), (float)n);
+#pragma unroll 1
+                        for (int k = 0; k < 2 && n > 1; ++k) {
+                            const float off = rintf((float)(long long)(rem - W.mass(j, w)) * ones);
+                            j = (uint32_t)min(max((long long)j + (long long)off, 1ll), (long long)n);
+                        }
+#pragma unroll 1
                         for (int k = 0; k < 4 && j > 1 && W.mass(j - 1, w) >= rem; ++k) --j;
+#pragma unroll 1
                         for (int k = 0; k < 4 && j < n && W.mass(j, w) < rem; ++k) ++j;
                     }
-                    const int src = __ffs(who) - 1;
-                    f.mass = __shfl_sync(0xffffffffu, before + W.mass(j, w), src);
-                    f.bits = __shfl_sync(0xffffffffu, bits, src);
-                    f.r = __shfl_sync(0xffffffffu, j - 1, src);
-                    f.w = __shfl_sync(0xffffffffu, w, src);
-                    break;
+                    sh.found = Found{before + W.mass(j, w), B::bits(o[0]), j - 1, n, w};
                 }
-                c0 += __shfl_sync(0xffffffffu, ci, 31);
-                m0 += __shfl_sync(0xffffffffu, mi, 31);
+                break;
             }
+            c0 += __shfl_sync(0xffffffffu, ci, 31);
+            m0 += __shfl_sync(0xffffffffu, mi, 31);
         }
-        if (wide) sync_warps();
-        return f;
+        __syncwarp();
     }
+    if (kWide) sync_warps();
+}
 
-    // Filters and draw, from the segments' sums.  As find() is called.
-    __device__ void choose(int i, float T) const {
-        Lane L = {};
-        if (threadIdx.x < 32) L = walk();
-        const float u = __ldg(P.u + i);
-        const float p = P.top_p ? __ldg(P.top_p + i) : 1.0f;
-        int k = P.top_k ? __ldg(P.top_k + i) : 0;
-        if (T == 0.0f) k = 1;
-        // the other warps (wide path) follow the walking one's branches
-        u64 kept = L.total_mass;
-        bool cut = k > 0 && (uint32_t)k < L.total_count;
-        if (wide) cut = share(cut);
-        if (cut) kept = find(L, true, (uint32_t)k).mass;
-        if (p < 1.0f) {
-            const double t = ceil((double)p * (double)kept);
-            const u64 target = t >= 1.0 ? min((u64)t, kept) : 1;
-            kept = min(kept, find(L, false, target).mass);
-        }
-        const double t = (double)u * (double)kept;
-        const u64 target = t >= 0.0 ? (t < (double)kept ? min((u64)t + 1, kept) : kept) : 1;
-        const Found f = find(L, false, target);
-        if (threadIdx.x == 0) {
-            sh.draw.bits = f.bits;
-            sh.draw.r = f.r;
-            sh.draw.prob = (float)((double)f.w * W.unit() / (double)kept);
-        }
-    }
-    __device__ bool share(bool v) const {
-        if (threadIdx.x == 0) sh.flag = v;
-        sync_warps();
-        v = sh.flag;
-        sync_warps();
-        return v;
-    }
+// x times v for 0 <= x < 1, rounded up or down; x < 0: 0.
+__device__ __forceinline__ u64 part_of(float x, u64 v, bool up) {
+    if (!(x > 0.0f)) return 0;
+    // x = c 2^-k, c < 2^24
+    const uint32_t b = __float_as_uint(x), e = b >> 23;
+    const u64 c = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const int k = 150 - (int)max(e, 1u);                   // >= 24
+    const u64 hi = __umul64hi(c, v), lo = c * v;           // hi < 2^24
+    if (k >= 88) return up ? 1 : 0;                        // c v < 2^88
+    const u64 q = k >= 64 ? hi >> (k - 64) : hi << (64 - k) | lo >> k;
+    const u64 left = k >= 64 ? (hi & ((1ull << (k - 64)) - 1)) | lo : lo & ((1ull << k) - 1);
+    return q + (up && left);
+}
 
-    // The wide path's segment sums: windows of keys from the maximum's down, as far as weights reach (every thread).
-    __device__ void sum_wide() const {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        u64* const mass = reinterpret_cast<u64*>(smem);
-        uint32_t* const count = reinterpret_cast<uint32_t*>(smem + kWideSegments * 8);
-        for (int s = threadIdx.x; s < kWideSegments; s += kThreads) {
-            mass[s] = 0;
-            count[s] = 0;
-        }
-        for (int o0 = 0; o0 < 65536; o0 += kWindow) {
-            // the window's first finite value is its largest: its last one is the smallest
-            const float last = __uint_as_float(bits_of(o0 + kWindow - 1) << 16), first = __uint_as_float(bits_of(o0) << 16);
-            if (last > W.m32) continue;                                        // all above the maximum
-            if (!isnan(first) && first < W.m32 && W.of(first, sh.powers) == 0) break;
-            count_keys(o0, kWindow);
-            for (int s = warp; s < kWindow / kWideSegment; s += kWarps) {
-                uint32_t c = 0;
-                u64 m = 0;
-                for (int b = lane; b < kWideSegment; b += 32) {
-                    const int o = s * kWideSegment + b;
-                    const uint32_t n = count_of(o);
-                    const u64 w = n ? W.of(__uint_as_float(bits_of(o0 + o) << 16), sh.powers) : 0;
-                    if (w) c += n;
-                    m += W.mass(n, w);
-                }
-                c = __reduce_add_sync(0xffffffffu, c);
-                m = warp_sum64(m);
-                if (lane == 0) {
-                    mass[o0 / kWideSegment + s] = m;
-                    count[o0 / kWideSegment + s] = c;
-                }
-            }
-            sync_warps();
-        }
-        sync_warps();
+// Filters and draw, from the segments' sums.  As find() is called.
+template <bool kWide>
+__device__ __noinline__ void choose(float u, int k, float p) {
+    using B = Bins<kWide>;
+    Shared& sh = shared();
+    u64 kept = B::seg_mass()[B::kCount - 1];
+    if (k > 0 && (uint32_t)k < B::seg_count()[B::kCount - 1]) {
+        find<kWide>(true, (uint32_t)k);
+        kept = sh.found.mass;
+        __syncwarp();
     }
+    if (p < 1.0f) {
+        find<kWide>(false, max(part_of(p, kept, true), 1ull));
+        kept = min(kept, sh.found.mass);
+        __syncwarp();
+    }
+    find<kWide>(false, u >= 0.0f ? (u < 1.0f ? min(part_of(u, kept, false) + 1, kept) : kept) : 1);
+    if (threadIdx.x == 0) sh.kept = kept;
+}
 
-    // Token number r (from the lowest) of those with value `bits` in [e0, e1), into P.tokens[i].  Every thread calls.
-    __device__ void locate(int i, uint32_t bits, long long r, int e0, int e1) const {
-        const uint32_t care = bits == 0 ? 0x7fffu : 0xffffu;
-        int span = e1 - e0;
-        for (;;) {
-            // gather the matches; too many for the list: a bucket of the range that holds the wanted one
-            const int per = max(8, ((span + kBuckets - 1) / kBuckets + 7) / 8 * 8);
-            for (int b = threadIdx.x; b < kBuckets; b += kThreads) sh.buckets[b] = 0;
-            if (threadIdx.x == 0) sh.count = 0;
-            sync_warps();
-            constexpr int kDeep = 8;   // 32 KB of the CTA's in flight
-            for (int e = e0 + (int)threadIdx.x * 8; e < e0 + span; e += kThreads * 8 * kDeep) {
-                uint4 q[kDeep];
-#pragma unroll
-                for (int d = 0; d < kDeep; ++d) {
-                    const int at = e + d * kThreads * 8;
-                    q[d] = at < e0 + span ? *reinterpret_cast<const uint4*>(x + at) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int d = 0; d < kDeep; ++d) {
-                    const int at = e + d * kThreads * 8;
-                    const uint32_t w[4] = {q[d].x, q[d].y, q[d].z, q[d].w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0);
-                        if (((b ^ bits) & care) == 0 && at + k < e0 + span) {
-                            const int slot = atomicAdd(&sh.count, 1);
-                            if (slot < kList) sh.list[slot] = at + k;
-                            atomicAdd(&sh.buckets[(at + k - e0) / per], 1);
-                        }
-                    }
-                }
+// The drawn token's w over the kept mass: the quotient of the leading 24 bits, made good by what they leave out.
+__device__ __forceinline__ float probability(u64 w, u64 kept, int shift) {
+    const float unit = __uint_as_float((uint32_t)(127 - shift) << 23);
+    const float a1 = (float)w * unit, a0 = (float)(long long)(w - (u64)((float)w)) * unit;
+    const float b1 = (float)kept, b0 = (float)(long long)(kept - (u64)b1);
+    const float q = a1 / b1;
+    return q + (fmaf(-q, b1, a1) + a0 - q * b0) / b1;
+}
+
+// The wide path's segment sums: windows of keys from the maximum's down, as far as weights reach (every thread).
+__device__ __noinline__ void sum_wide() {
+    using B = Bins<true>;
+    Shared& sh = shared();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Weights W = sh.row.W;
+    for (int s = threadIdx.x; s < B::kCount; s += kThreads) {
+        B::seg_mass()[s] = 0;
+        B::seg_count()[s] = 0;
+    }
+#pragma unroll 1
+    for (int o0 = 0; o0 < 65536; o0 += kWindow) {
+        // the window's first finite value is its largest, its last one the smallest
+        const float last = B::value(o0 + kWindow - 1), first = B::value(o0);
+        if (last > W.m) continue;                                           // all above the maximum
+        if (!isnan(first) && first < W.m && W.of(first, sh.powers) == 0) break;
+        count_keys(o0, kWindow);
+#pragma unroll 1
+        for (int s = warp; s < kWindow / B::kSize; s += kWarps) {
+            uint32_t c = 0;
+            u64 m = 0;
+#pragma unroll 1
+            for (int o = s * B::kSize + lane; o < (s + 1) * B::kSize; o += 32) {
+                const uint32_t n = word_at(kNegative + o * 4);
+                const u64 w = n ? W.of(B::value(o0 + o), sh.powers) : 0;
+                if (w) c += n;
+                m += W.mass(n, w);
             }
-            sync_warps();
-            const int n = sh.count;
-            if (n <= kList || per == 8) break;
-            if (threadIdx.x == 0) {
-                int b = 0;
-                while (b + 1 < kBuckets && r >= sh.buckets[b]) r -= sh.buckets[b++];
-                sh.segment = b;
-                sh.draw.r = r;
+            c = __reduce_add_sync(0xffffffffu, c);
+            m = warp_sum64(m);
+            if (lane == 0) {
+                B::seg_mass()[o0 / B::kSize + s] = m;
+                B::seg_count()[o0 / B::kSize + s] = c;
             }
-            sync_warps();
-            e0 += sh.segment * per;
-            span = min(per, e1 - e0);
-            r = sh.draw.r;
-            sync_warps();
-        }
-        const int n = min(sh.count, kList);
-        for (int a = threadIdx.x; a < n; a += kThreads) {
-            const int mine = sh.list[a];
-            int before = 0;
-            for (int b = 0; b < n; ++b) before += sh.list[b] < mine;
-            if (before == r) P.tokens[i] = mine;
         }
         sync_warps();
     }
-};
+    sync_warps();
+}
+
+// Which of the first `have` halves of four words are 0, a bit each.
+__device__ __noinline__ uint32_t zero_halves(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int have) {
+    uint32_t h = (a & 0xffffu) == 0 | (a >> 16 == 0) << 1 | ((b & 0xffffu) == 0) << 2 | (b >> 16 == 0) << 3;
+    h |= ((c & 0xffffu) == 0) << 4 | (c >> 16 == 0) << 5 | ((d & 0xffffu) == 0) << 6 | (d >> 16 == 0) << 7;
+    return have < 8 ? h & ((1u << have) - 1u) : h;
+}
+
+// Token number r (from the lowest) of the n with value `bits` in values [e0, e1) of x; `token` is where it goes.  Every
+// thread calls.  A pass takes 16384 values in their order (piece d of 4, thread, value) and counts the matches; the pass
+// that reaches r is resolved.  From the slice's end, whose values came last: what L2 holds of the rows in flight (304 of
+// 300 KB) is their later part.
+__device__ __noinline__ void locate(const uint16_t* x, int* token, uint32_t bits, uint32_t r, uint32_t n, int e0, int e1) {
+    Shared& sh = shared();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t both = bits | bits << 16, care = bits == 0 ? 0x7fff7fffu : 0xffffffffu;
+    constexpr int kDeep = 4, kPass = kThreads * 8 * kDeep;   // 32 KB of the CTA's in flight
+    uint32_t behind = n - 1 - r;                             // matches behind the wanted one
+    if (tid < 3) sh.counts[tid] = 0;
+    sync_warps();
+#pragma unroll 1
+    for (int e = e0 + (e1 - e0 - 1) / kPass * kPass, pass = 0; e >= e0; e -= kPass, pass = pass == 2 ? 0 : pass + 1) {
+        uint4 q[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int at = e + (d * kThreads + tid) * 8;
+            q[d] = at < e1 ? __ldg(reinterpret_cast<const uint4*>(x + at)) : make_uint4(~both, ~both, ~both, ~both);
+        }
+        uint32_t hit = 0;   // 8 bits of a piece each
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            // a half that is 0 after the xor is one whose borrow sets its top bit; the halves are looked at only then
+            const uint32_t t[4] = {(q[d].x ^ both) & care, (q[d].y ^ both) & care, (q[d].z ^ both) & care,
+                                   (q[d].w ^ both) & care};
+            const uint32_t any = (((t[0] - 0x00010001u) & ~t[0]) | ((t[1] - 0x00010001u) & ~t[1]) |
+                                  ((t[2] - 0x00010001u) & ~t[2]) | ((t[3] - 0x00010001u) & ~t[3])) & 0x80008000u;
+            if (any) hit |= zero_halves(t[0], t[1], t[2], t[3], e1 - (e + (d * kThreads + tid) * 8)) << (d * 8);
+        }
+        if (hit) atomicAdd(&sh.counts[pass], __popc(hit));
+        if (tid == 0) sh.counts[pass == 2 ? 0 : pass + 1] = 0;
+        sync_warps();
+        const uint32_t all = sh.counts[pass];
+        if (behind >= all) {
+            behind -= all;
+            continue;
+        }
+        r = all - 1 - behind;
+        // 64 groups in order: piece d, warp
+        static_assert(kDeep * kWarps == 64, "two groups a lane");
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const uint32_t c = __reduce_add_sync(0xffffffffu, __popc(hit >> (d * 8) & 0xffu));
+            if (lane == 0) sh.groups[d * kWarps + warp] = c;
+        }
+        sync_warps();
+        auto before_of = [&](uint32_t c) {   // sum over the lanes before this one
+            uint32_t s = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, s, off);
+                if (lane >= off) s += y;
+            }
+            return s - c;
+        };
+        const uint32_t g0 = sh.groups[2 * lane], g1 = sh.groups[2 * lane + 1];
+        const uint32_t start = before_of(g0 + g1);
+        const int src = 31 - __clz(__ballot_sync(0xffffffffu, start <= r && g0 + g1 > 0));   // its pair of groups
+        const uint32_t left = r - __shfl_sync(0xffffffffu, start, src), of0 = __shfl_sync(0xffffffffu, g0, src);
+        const int g = 2 * src + (left >= of0);
+        const uint32_t want = left >= of0 ? left - of0 : left;   // within the group
+        if (g % kWarps == warp) {
+            const int d = g / kWarps;
+            uint32_t h = hit >> (d * 8) & 0xffu;
+            const uint32_t before = before_of(__popc(h));
+            if (want >= before && want < before + __popc(h)) {
+#pragma unroll 1
+                for (uint32_t k = before; k < want; ++k) h &= h - 1;
+                *token = e + (d * kThreads + tid) * 8 + __ffs(h) - 1;
+            }
+        }
+        break;
+    }
+    sync_warps();
+}
 
 // One 16-byte piece: its values into the counters, its maximum into `top`.
 __device__ __forceinline__ void count_word(uint32_t w, uint32_t base, uint32_t& top) {
@@ -606,8 +686,7 @@ __device__ __forceinline__ void count_word(uint32_t w, uint32_t base, uint32_t& 
 }
 
 __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __grid_constant__ SampleParams P) {
-    extern __shared__ __align__(128) unsigned char smem[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem + kGap);
+    Shared& sh = shared();
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -619,7 +698,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         for (int k = 0; k < 2; ++k) mbar_init(smem_addr(&sh.meet[k]), P.cluster);
         mbar_fence_init();
     }
-    if (tid < 64) sh.powers[tid >> 4][tid & 15] = c_powers.t[tid >> 4][tid & 15];
+    if (tid < kPowers) sh.powers[tid] = c_powers.t[tid];
     __syncthreads();
     const int ctas = P.cluster;
     if (ctas > 1) cluster_sync();
@@ -643,6 +722,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
             for (int i = first; i < P.N && !lost; i += step) {
                 const uint16_t* const x = row_of(i);
                 if (!x) continue;
+#pragma unroll 1
                 for (int c = 0; c < chunks; ++c, ++n) {
                     const uint32_t k = n % kStages;
                     if (!mbar_wait_bounded(smem_addr(&sh.empty[k]), (n / kStages & 1) ^ 1, kWaitNs) ||
@@ -673,6 +753,10 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
             }
             continue;
         }
+        const float T = P.temperature ? __ldg(P.temperature + i) : 1.0f, u = __ldg(P.u + i);
+        const float p = P.top_p ? __ldg(P.top_p + i) : 1.0f, min_p = P.min_p ? __ldg(P.min_p + i) : 0.0f;
+        const int k = P.top_k ? __ldg(P.top_k + i) : 0;
+#pragma unroll 1
         for (uint32_t at = tid * 16; at < (kValues + 1) * 4; at += kThreads * 16) {
             // the last piece may reach into the word behind, which is padding on both sides
             *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
@@ -680,40 +764,39 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         }
         sync_warps();
         uint32_t top = 0xff80ff80u;
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c, ++n) {
-            const uint32_t k = n % kStages;
+            const uint32_t stage = n % kStages;
             if (*(volatile int*)&sh.abort == 0 &&
-                !mbar_wait_bounded(smem_addr(&sh.full[k]), n / kStages & 1, kWaitNs)) {
+                !mbar_wait_bounded(smem_addr(&sh.full[stage]), n / kStages & 1, kWaitNs)) {
                 set_error(P.err, DLLM_DEVERR_TIMEOUT);
                 *(volatile int*)&sh.abort = 1;
             }
             const int left = e1 - (e0 + c * kChunk);
-            const uint4* const in = reinterpret_cast<const uint4*>(smem + kRing + k * kChunk * 2);
+            const uint4* const in = reinterpret_cast<const uint4*>(smem + kRing + stage * kChunk * 2);
             constexpr int kPieces = kChunk / 8 / kThreads;
             uint4 q[kPieces];
 #pragma unroll
             for (int d = 0; d < kPieces; ++d) q[d] = in[d * kThreads + tid];
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.empty[k]));
-            if (left >= kChunk) {
-#pragma unroll
-                for (int d = 0; d < kPieces; ++d) {
-                    count_word(q[d].x, base, top);
-                    count_word(q[d].y, base, top);
-                    count_word(q[d].z, base, top);
-                    count_word(q[d].w, base, top);
-                }
-            } else {
+            if (lane == 0) mbar_arrive(smem_addr(&sh.empty[stage]));
+            if (left < kChunk) {   // -inf behind the slice's end
 #pragma unroll
                 for (int d = 0; d < kPieces; ++d) {
                     const int have = left - (d * kThreads + tid) * 8;   // values of this piece
-                    const uint32_t w[4] = {q[d].x, q[d].y, q[d].z, q[d].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (2 * j + 1 < have) count_word(w[j], base, top);
-                        else if (2 * j < have) count_word((w[j] & 0xffffu) | 0xff800000u, base, top);   // counted as low
-                    }
+                    q[d].x = have > 1 ? q[d].x : (q[d].x & 0xffffu) | 0xff800000u;
+                    q[d].y = have > 3 ? q[d].y : have > 2 ? (q[d].y & 0xffffu) | 0xff800000u : 0xff80ff80u;
+                    q[d].z = have > 5 ? q[d].z : have > 4 ? (q[d].z & 0xffffu) | 0xff800000u : 0xff80ff80u;
+                    q[d].w = have > 7 ? q[d].w : have > 6 ? (q[d].w & 0xffffu) | 0xff800000u : 0xff80ff80u;
                 }
+            }
+#pragma unroll
+            for (int d = 0; d < kPieces; ++d) {
+                if ((d * kThreads + tid) * 8 >= left) break;
+                count_word(q[d].x, base, top);
+                count_word(q[d].y, base, top);
+                count_word(q[d].z, base, top);
+                count_word(q[d].w, base, top);
             }
         }
         // what the slice holds besides the counted values
@@ -723,11 +806,12 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         if (lane == 0) sh.part[warp] = m;
         if (tid == 0) sh.flag = 0;
         sync_warps();
-        const uint32_t* const pos = reinterpret_cast<const uint32_t*>(smem);
-        const uint32_t* const neg = reinterpret_cast<const uint32_t*>(smem + kNegative);
+        uint32_t* const pos = reinterpret_cast<uint32_t*>(smem);
+        uint32_t* const neg = reinterpret_cast<uint32_t*>(smem + kNegative);
         const bool zeros = pos[0] + neg[0] > 0;
         if (zeros) {   // exact zeros, or small values that only the wide path tells apart
             bool small = false;
+#pragma unroll 1
             for (int e = e0 + tid * 8; e < e1; e += kThreads * 8) {
                 const uint4 q = *reinterpret_cast<const uint4*>(x + e);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -746,8 +830,10 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) f.max = max_nan(f.max, sh.part[w]);
             f.other = sh.flag | (pos[kValues] > 0);
-            f.low = (int)neg[kValues] - (e1 == P.V && e1 > e0 ? P.V & 1 : 0);   // the odd last value's partner
+            f.low = (int)neg[kValues] - ((e0 - e1) & 7);   // without what fills the last piece
             sh.facts = f;
+            pos[0] += neg[0];   // -0 is 0
+            neg[0] = 0;
         }
         if (ctas > 1) {
             meeting.arrive();
@@ -759,45 +845,57 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         if (ctas > 1) {
             const uint32_t at = smem_addr(&sh.facts);
             all = SliceFacts{-INFINITY, 0, 0};
+#pragma unroll 1
             for (int q = 0; q < ctas; ++q) {
                 all.max = max_nan(all.max, __uint_as_float(peer_load(at, q)));
                 all.other |= (int)peer_load(at + 4, q);
                 all.low += (int)peer_load(at + 8, q);
             }
         }
-        const float T = P.temperature ? __ldg(P.temperature + i) : 1.0f;
         const bool ok = isfinite(all.max) && T >= 0.0f;
-        Row R{P, sh, smem, base, x, Weights{}, false};
-        R.W.m32 = all.max;
-        R.W.m = all.max;
-        R.W.s = T > 0.0f ? 1.4426950408889634 / (double)T : 1.0;
-        R.W.s32 = (float)fmin(R.W.s, 3e38);
-        R.W.shift = P.shift;
-        R.W.least = 0;
-        if (P.min_p && T > 0.0f) {
-            const float least = __ldg(P.min_p + i);
-            if (least > 0.0f) R.W.least = (u64)ceil(fmin((double)least, 1.0) * 4611686018427387904.0);
-        }
+        Weights W;
+        W.shift = P.shift;
+        W.set(all.max, T == 0.0f ? 1.0f : T, T == 0.0f ? 0.0f : min_p);
         // low values count where their weights do: -256 is the largest
-        R.wide = all.other || (all.low > 0 && (-256.0f - all.max) * R.W.s32 > -80.0f);
-        if (ok && !R.wide) {
-            for (int s = rank * kWarps + warp; s < kSegments; s += ctas * kWarps) {
-                const int o = s * 32 + lane;
-                uint32_t c = R.count_of(o);
-                u64 mass = 0;
-                if (__any_sync(0xffffffffu, c > 0)) {
-                    const u64 w = c ? R.W.of(__uint_as_float(R.bits_of(o) << 16), sh.powers) : 0;
-                    if (w == 0) c = 0;
-                    mass = warp_sum64(R.W.mass(c, w));
-                    c = __reduce_add_sync(0xffffffffu, c);
+        const bool wide = all.other || (all.low > 0 && W.rough(-256.0f) > -80.0f);
+        if (tid == 0) sh.row = RowFacts{W, x, P.V, ctas};
+        if (ok && !wide) {
+            // Sums of the segments, a warp 2 neighbouring ones at a time: the weights' chains of operations run side by side
+            constexpr int kGroup = 2;
+            static_assert(kSegments % kGroup == 0, "whole groups");
+#pragma unroll 1
+            for (int g = rank * kWarps + warp; g * kGroup < kSegments; g += ctas * kWarps) {
+                int o[kGroup];
+                uint32_t c[kGroup], any = 0;
+                u64 mass[kGroup] = {};
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) o[j] = (g * kGroup + j) * 32 + lane;
+                counts_of(o, c, ctas);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) any |= c[j];
+                if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j) {
+                        const u64 w = W.of(Bins<false>::value(o[j]), sh.powers);
+                        if (w == 0) c[j] = 0;
+                        mass[j] = W.mass(c[j], w);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j) {
+                        c[j] = __reduce_add_sync(0xffffffffu, c[j]);
+                        mass[j] = warp_sum64(mass[j]);
+                    }
                 }
-                if (lane == 0) {
+                if (lane < kGroup) {
+                    const uint32_t count = lane ? c[1] : c[0];
+                    const u64 m = lane ? mass[1] : mass[0];
+                    const int seg = g * kGroup + lane;
                     if (ctas > 1) {
-                        peer_store(smem_addr(&sh.seg_count[s]), 0, c);
-                        peer_store64(smem_addr(&sh.seg_mass[s]), 0, mass);
+                        peer_store(smem_addr(&sh.seg_count[seg]), 0, count);
+                        peer_store64(smem_addr(&sh.seg_mass[seg]), 0, m);
                     } else {
-                        sh.seg_count[s] = c;
-                        sh.seg_mass[s] = mass;
+                        sh.seg_count[seg] = count;
+                        sh.seg_mass[seg] = m;
                     }
                 }
             }
@@ -808,11 +906,14 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         } else {
             sync_warps();
         }
-        if (rank == 0) {
-            if (ok && !R.wide && warp == 0) R.choose(i, T);
-            if (ok && R.wide) {
-                R.sum_wide();
-                R.choose(i, T);
+        if (rank == 0 && ok) {
+            if (!wide) {
+                add_up<false>();
+                if (warp == 0) choose<false>(u, T == 0.0f ? 1 : k, p);
+            } else {
+                sum_wide();
+                add_up<true>();
+                choose<true>(u, T == 0.0f ? 1 : k, p);
             }
         }
         if (ctas > 1) {
@@ -821,32 +922,33 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         } else {
             sync_warps();
         }
-        Draw d = sh.draw;
+        uint32_t bits = sh.found.bits, r = sh.found.r, count = sh.found.n;
         int l0 = e0, l1 = e1;
-        bool mine = ok && (rank == 0 || !R.wide);
-        if (ctas > 1 && !(ok && R.wide)) {
-            if (ok) {
-                const uint32_t at = smem_addr(&sh.draw);
-                d.bits = peer_load(at + offsetof(Draw, bits), 0);
-                d.r = peer_load(at + offsetof(Draw, r), 0);
-                const uint32_t c4 = (d.bits & 0x7fffu) == 0 ? 0 : ((d.bits & 0x7fffu) - kLow) * 4;
-                for (int q = 0; q <= rank; ++q) {
-                    uint32_t c = peer_load(base + (d.bits & 0x8000u ? kNegative : 0u) + c4, q);
-                    if (c4 == 0) c += peer_load(base + kNegative, q);
-                    if (q < rank) d.r -= c;
-                    else mine = d.r >= 0 && d.r < (long long)c;
-                }
-            }
-        } else if (ok && R.wide) {
+        bool mine = ok && (rank == 0 || !wide);
+        if (wide) {
             l0 = 0;
             l1 = P.V;
+        } else if (ctas > 1 && ok) {
+            // the slice that holds the token
+            const uint32_t at = smem_addr(&sh.found);
+            bits = peer_load(at + offsetof(Found, bits), 0);
+            r = peer_load(at + offsetof(Found, r), 0);
+            mine = false;
+            const uint32_t counter = (bits & 0x8000u ? kNegative : 0u) + ((bits & 0x7fffu) == 0 ? 0 : ((bits & 0x7fffu) - kLow) * 4);
+#pragma unroll 1
+            for (int q = 0; q <= rank; ++q) {
+                const uint32_t c = peer_load(base + counter, q);
+                if (q == rank) mine = r < (count = c);
+                else if (r >= c) r -= c;
+                else break;   // a slice before this one
+            }
         }
         if (ctas > 1) meeting.arrive();   // this CTA has read the others' counters
-        if (rank == 0 && tid == 0) {
-            P.prob[i] = ok ? sh.draw.prob : __int_as_float(0x7fc00000);
+        if (rank == 0 && tid == kThreads - 32) {
+            P.prob[i] = ok ? probability(sh.found.w, sh.kept, P.shift) : __int_as_float(0x7fc00000);
             if (!ok) P.tokens[i] = -1;
         }
-        if (mine) R.locate(i, d.bits, d.r, l0, l1);
+        if (mine) locate(x, P.tokens + i, bits, r, count, l0, l1);
         if (ctas > 1) meeting.wait(&sh.abort, P.err);
         else sync_warps();
     }

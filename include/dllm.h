@@ -938,7 +938,7 @@ int dllm_kv4_evict(const dllm_kv4_evict_args* args, void* stream);
  * Cumulative masses are held to about 2^-40 of the whole (64-bit fixed point
  * over the counts of a row's different values), whatever V: the draw is the
  * definition's but where u lies that close to a border.  Tokens with weights
- * below 2^-75 of the largest are not drawn.  A row's result depends on that row
+ * below 2^-62 of the largest are not drawn.  A row's result depends on that row
  * alone.  Serves sampling: no gradient. */
 typedef struct dllm_sample_args {
     int32_t N;                  /* entries (>= 0) */
