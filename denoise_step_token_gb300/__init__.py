@@ -20,6 +20,9 @@ Names follow the C ABI in ``include/dllm.h``:
   cache of keys and values in 4 bits: its pool, the write, a block's
   attention over it, and its thinning by attention weight.
 * ``sample`` -- tokens drawn from the step's logits by given random numbers.
+* ``page_fork`` / ``page_grow`` / ``page_free`` / ``page_copy`` /
+  ``page_compact`` -- who holds which pages of a cache: shared prefixes, new
+  pages, release, copies between pools, and the closing of a pool's gaps.
 """
 from __future__ import annotations
 
@@ -34,6 +37,7 @@ from . import _build
 
 __all__ = ["load", "step", "step_host", "features", "pack_plan", "admit", "pack", "advance", "compact", "refill",
            "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict", "sample",
+           "page_fork", "page_grow", "page_free", "page_copy", "page_compact",
            "get_device_error", "DllmError", "NUM_FEATURES", "LIB_PATH"]
 
 LIB_PATH = _build.LIB_PATH
@@ -147,6 +151,19 @@ class SampleArgs(ctypes.Structure):
                 ("temperature", _p), ("top_k", _p), ("top_p", _p), ("min_p", _p), ("tokens", _p), ("prob", _p)]
 
 
+PAGES_MAX_ARRAYS = 64
+
+
+class PagesPool(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("n_arrays", _i32), ("arrays", _p * PAGES_MAX_ARRAYS),
+                ("page_bytes", _i64 * PAGES_MAX_ARRAYS)]
+
+
+class PagesBatch(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("B", _i32), ("max_pages", _i32), ("page_size", _i32), ("refs", _p), ("table", _p),
+                ("held", _p)]
+
+
 MAX_TOP = 32
 KV4_GROUP = 32
 
@@ -212,6 +229,13 @@ _SIGNATURES = {
     "dllm_kv4_attend": (ctypes.c_int, [ctypes.POINTER(Kv4AttendArgs), _p]),
     "dllm_kv4_evict": (ctypes.c_int, [ctypes.POINTER(Kv4EvictArgs), _p]),
     "dllm_sample": (ctypes.c_int, [ctypes.POINTER(SampleArgs), _p]),
+    "dllm_pages_workspace_size": (_sz, [_i32, _i32]),
+    "dllm_pages_copy": (ctypes.c_int, [ctypes.POINTER(PagesPool), ctypes.POINTER(PagesPool), _i32, _p, _p, _p]),
+    "dllm_pages_fork": (ctypes.c_int, [ctypes.POINTER(PagesBatch), ctypes.POINTER(PagesPool), _p, _i32, _p, _p, _p, _p,
+                                       _sz, _p]),
+    "dllm_pages_grow": (ctypes.c_int, [ctypes.POINTER(PagesBatch), _p, _i32, _p, _i32, _p, _p, _sz, _p]),
+    "dllm_pages_free": (ctypes.c_int, [ctypes.POINTER(PagesBatch), _i32, _p, _p]),
+    "dllm_pages_compact": (ctypes.c_int, [ctypes.POINTER(PagesBatch), ctypes.POINTER(PagesPool), _p, _p, _p, _sz, _p]),
 }
 
 
@@ -249,7 +273,7 @@ def load(build=True):
             raise RuntimeError(f"libdllm ABI version {lib.dllm_abi_version()}, binding expects {ABI_VERSION}")
         for which, cls in enumerate((StepArgs, PackArgs, CompactArgs, AdvanceArgs, RefillArgs, LoopConfig, LoopInfo,
                                      VocabShard, LoopControl, LogprobsArgs, Kv4Cache, Kv4WriteArgs, Kv4AttendArgs,
-                                     Kv4EvictArgs, SampleArgs)):
+                                     Kv4EvictArgs, SampleArgs, PagesPool, PagesBatch)):
             if lib.dllm_struct_size(which) != ctypes.sizeof(cls):
                 raise RuntimeError(f"ABI mismatch for {cls.__name__}: library {lib.dllm_struct_size(which)} "
                                    f"bytes, binding {ctypes.sizeof(cls)}")
@@ -1040,4 +1064,153 @@ def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=
     rc = (_lib or load()).dllm_sample(ctypes.byref(a), _raw_stream(torch, dev))
     if rc:
         _check("dllm_sample", rc)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# pages of a cache
+# ---------------------------------------------------------------------------
+def _pages_pool(torch, dev, pools):
+    """The pool's arrays: tensors whose first dimension counts its pages."""
+    n = len(pools)
+    if n > PAGES_MAX_ARRAYS:
+        raise ValueError(f"a pool has at most {PAGES_MAX_ARRAYS} arrays")
+    _check_tensors(torch, dev, *pools)
+    n_pages = pools[0].shape[0] if n and pools[0].dim() else 0
+    a = PagesPool(n_pages, n)
+    for k, t in enumerate(pools):
+        if t.dim() < 1 or t.shape[0] != n_pages or n_pages < 1:
+            raise ValueError("every array of a pool needs its pages as the first dimension")
+        a.arrays[k] = t.data_ptr()
+        a.page_bytes[k] = t.numel() // n_pages * t.element_size()
+    return a
+
+
+def _pages_batch(torch, refs, table, held, page_size):
+    dev = refs.device
+    _check_tensors(torch, dev, refs, table, held)
+    int32 = torch.int32
+    if refs.dtype != int32 or refs.dim() != 1:
+        raise TypeError("refs must be int32 [n_pages]")
+    if table.dtype != int32 or table.dim() != 2:
+        raise TypeError("the page table must be int32 [B, max_pages]")
+    B, most = table.shape
+    if held.dtype != int32 or held.numel() != B:
+        raise TypeError(f"held must be int32 [{B}]")
+    return PagesBatch(refs.numel(), B, most, page_size, refs.data_ptr(), table.data_ptr(), held.data_ptr())
+
+
+def _pages_rows(torch, dev, name, t):
+    _check_tensors(torch, dev, t)
+    if t.dtype != torch.int32 or t.dim() != 1:
+        raise TypeError(f"{name} must be int32 [n]")
+    return t.numel()
+
+
+def _pages_workspace(torch, lib, dev, n_pages, entries):
+    return torch.empty(int(lib.dllm_pages_workspace_size(n_pages, entries)), dtype=torch.uint8, device=dev)
+
+
+def page_fork(pools, refs, table, held, lens, src, dst, *, page_size):
+    """Fork requests (dllm_pages_fork) on the current stream: row ``dst[f]``
+    becomes a copy of row ``src[f]``; full pages are shared, a last page that
+    is not full is copied to a free one.
+
+    pools: the cache's tensors, each with the pages as its first dimension
+           (every layer's pages and weights)
+    refs:  int32 [n_pages] holders of each page (updated)
+    table: int32 [B, max_pages]; held, lens: int32 [B] pages and tokens of each
+           request (all updated for the rows ``dst``, which must hold none)
+    src, dst: int32 [F]; no dst twice, none among the src
+    Returns int32 [F]: the page each fork took, -1 none, -2 not served."""
+    torch = _torch()
+    dev = refs.device
+    batch = _pages_batch(torch, refs, table, held, page_size)
+    pool = _pages_pool(torch, dev, pools)
+    F = _pages_rows(torch, dev, "src", src)
+    if _pages_rows(torch, dev, "dst", dst) != F:
+        raise ValueError("one dst for every src")
+    _check_tensors(torch, dev, lens)
+    if not pools:
+        pool.n_pages = batch.n_pages
+    fresh = torch.empty(F, dtype=torch.int32, device=dev)
+    lib = _lib or load()
+    stream = _raw_stream(torch, dev)
+    ws = _pages_workspace(torch, lib, dev, batch.n_pages, F)
+    rc = lib.dllm_pages_fork(ctypes.byref(batch), ctypes.byref(pool), _int32_rows(torch, "lens", lens, batch.B), F,
+                             src.data_ptr(), dst.data_ptr(), fresh.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    if rc:
+        _check("dllm_pages_fork", rc)
+    return fresh
+
+
+def page_grow(refs, table, held, lens, rows, extra, *, page_size):
+    """Give requests ``rows`` (int32 [R], none twice) free pages until they hold
+    those of ``lens[row] + extra`` tokens (dllm_pages_grow) on the current
+    stream.  Returns int32 [R]: the pages each took, -1 not served."""
+    torch = _torch()
+    dev = refs.device
+    batch = _pages_batch(torch, refs, table, held, page_size)
+    R = _pages_rows(torch, dev, "rows", rows)
+    _check_tensors(torch, dev, lens)
+    taken = torch.empty(R, dtype=torch.int32, device=dev)
+    lib = _lib or load()
+    stream = _raw_stream(torch, dev)
+    ws = _pages_workspace(torch, lib, dev, batch.n_pages, R)
+    rc = lib.dllm_pages_grow(ctypes.byref(batch), _int32_rows(torch, "lens", lens, batch.B), R, rows.data_ptr(), extra,
+                             taken.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    if rc:
+        _check("dllm_pages_grow", rc)
+    return taken
+
+
+def page_free(refs, table, held, rows):
+    """Give back all pages of requests ``rows`` (int32 [R]; dllm_pages_free) on
+    the current stream: refs of each less one, held 0."""
+    torch = _torch()
+    batch = _pages_batch(torch, refs, table, held, 1)
+    R = _pages_rows(torch, refs.device, "rows", rows)
+    rc = (_lib or load()).dllm_pages_free(ctypes.byref(batch), R, rows.data_ptr(), _raw_stream(torch, refs.device))
+    if rc:
+        _check("dllm_pages_free", rc)
+
+
+def page_copy(pools, to, src, dst):
+    """Copy pages ``src`` (int32 [n]) of one cache's tensors to pages ``dst`` of
+    another's, in the same order (dllm_pages_copy) on the current stream; -1
+    skips.  No dst twice, none among the src of the same pool."""
+    torch = _torch()
+    if not pools or len(pools) != len(to):
+        raise ValueError("both pools need the same arrays")
+    dev = pools[0].device
+    a, b = _pages_pool(torch, dev, pools), _pages_pool(torch, dev, to)
+    n = _pages_rows(torch, dev, "src", src)
+    if _pages_rows(torch, dev, "dst", dst) != n:
+        raise ValueError("one dst for every src")
+    rc = (_lib or load()).dllm_pages_copy(ctypes.byref(a), ctypes.byref(b), n, src.data_ptr(), dst.data_ptr(),
+                                          _raw_stream(torch, dev))
+    if rc:
+        _check("dllm_pages_copy", rc)
+
+
+def page_compact(pools, refs, table, held):
+    """Close a pool's gaps (dllm_pages_compact) on the current stream: with U
+    pages in use, those from U on move into the free ones below U; ``table`` and
+    ``refs`` follow.  Returns a dict: used (int32 [1], U) and map (int32
+    [n_pages], where each used page is now, -1 for a free one)."""
+    torch = _torch()
+    dev = refs.device
+    batch = _pages_batch(torch, refs, table, held, 1)
+    pool = _pages_pool(torch, dev, pools)
+    if not pools:
+        pool.n_pages = batch.n_pages
+    out = {"used": torch.empty(1, dtype=torch.int32, device=dev),
+           "map": torch.empty(batch.n_pages, dtype=torch.int32, device=dev)}
+    lib = _lib or load()
+    stream = _raw_stream(torch, dev)
+    ws = _pages_workspace(torch, lib, dev, batch.n_pages, 0)
+    rc = lib.dllm_pages_compact(ctypes.byref(batch), ctypes.byref(pool), out["used"].data_ptr(), out["map"].data_ptr(),
+                                ws.data_ptr(), ws.numel(), stream)
+    if rc:
+        _check("dllm_pages_compact", rc)
     return out

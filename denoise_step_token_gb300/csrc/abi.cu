@@ -110,6 +110,8 @@ extern "C" size_t dllm_struct_size(int which) {
         case 12: return sizeof(dllm_kv4_attend_args);
         case 13: return sizeof(dllm_kv4_evict_args);
         case 14: return sizeof(dllm_sample_args);
+        case 15: return sizeof(dllm_pages_pool);
+        case 16: return sizeof(dllm_pages_batch);
         default: return 0;
     }
 }

@@ -78,8 +78,8 @@ int dllm_last_cuda_error(const char** name);
  * 3 dllm_advance_args, 4 dllm_refill_args, 5 dllm_loop_config,
  * 6 dllm_loop_info_t, 7 dllm_vocab_shard, 8 dllm_loop_control,
  * 9 dllm_logprobs_args, 10 dllm_kv4_cache, 11 dllm_kv4_write_args,
- * 12 dllm_kv4_attend_args, 13 dllm_kv4_evict_args, 14 dllm_sample_args.
- * Returns 0 for an unknown `which`. */
+ * 12 dllm_kv4_attend_args, 13 dllm_kv4_evict_args, 14 dllm_sample_args,
+ * 15 dllm_pages_pool, 16 dllm_pages_batch.  Returns 0 for an unknown `which`. */
 size_t dllm_struct_size(int which);
 
 /* Fault injection for tests of the status plumbing (host only; nothing
@@ -958,6 +958,78 @@ typedef struct dllm_sample_args {
 
 /* Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
 int dllm_sample(const dllm_sample_args* args, void* stream);
+
+/* ======================================================================
+ * Pages of a cache: who holds which.  For the 4-bit cache (dllm_kv4_*) and any
+ * other whose pages lie one after the other in its pools: every layer's codes
+ * and attention weights are one array each of a pool, all with the same page
+ * numbers.
+ *
+ * refs[page] counts the requests that hold a page; a page with none is free.
+ * Request b holds the pages table[b][0 .. held[b]).  Free pages are handed out
+ * lowest first, to entries in their order.  Row, page or token counts outside
+ * the batch or pool, and too few free pages, set DLLM_DEVERR_PAGE; nothing
+ * outside the arrays is touched.  The calls only order whole numbers and bytes:
+ * equal calls give equal results.
+ * ====================================================================== */
+#define DLLM_PAGES_MAX_ARRAYS 64
+typedef struct dllm_pages_pool {
+    int32_t n_pages;            /* >= 1 */
+    int32_t n_arrays;           /* 0..DLLM_PAGES_MAX_ARRAYS */
+    void* arrays[DLLM_PAGES_MAX_ARRAYS];          /* device, 16-byte aligned: [n_pages][page_bytes] */
+    int64_t page_bytes[DLLM_PAGES_MAX_ARRAYS];    /* multiples of 16 */
+} dllm_pages_pool;
+typedef struct dllm_pages_batch {
+    int32_t n_pages;            /* of the pool (>= 1) */
+    int32_t B;                  /* requests (>= 0) */
+    int32_t max_pages;          /* table entries per request, 1..2^20 */
+    int32_t page_size;          /* tokens of a page (>= 1) */
+    int32_t* refs;              /* device [n_pages], 16-byte aligned */
+    int32_t* table;             /* device [B][max_pages] */
+    int32_t* held;              /* device [B] */
+} dllm_pages_batch;
+
+/* Workspace bytes of a call on a pool of n_pages pages with `entries` forks or
+ * rows (16-byte aligned, contents of no matter; one call at a time). */
+size_t dllm_pages_workspace_size(int32_t n_pages, int32_t entries);
+
+/* Copy page src[i] of one pool's arrays to page dst[i] of another's (the same
+ * pool will do; arrays in the same order with the same page_bytes).  -1 on
+ * either side: skip.  No dst twice, and none among the src of the same pool. */
+int dllm_pages_copy(const dllm_pages_pool* from, const dllm_pages_pool* to, int32_t n, const int32_t* src,
+                    const int32_t* dst, void* stream);
+
+/* Fork requests: row dst[f] becomes a copy of row src[f], with its lens[src[f]]
+ * tokens.  Full pages are shared; the last one, where it is not full, is copied
+ * to a free page, so that both may be written on.  held[dst[f]] is the pages of
+ * those tokens, lens[dst[f]] = lens[src[f]]; what dst[f] held before must have
+ * been freed.  fresh[f] = the page taken, -1 where the tokens end with a page;
+ * -2 for a fork that is not served (a row or page out of range, or no page left
+ * for it: then none of the later ones that need a page is served either): its
+ * lens and held become 0.  No dst twice, and none among the src; a src may
+ * occur any number of times. */
+int dllm_pages_fork(const dllm_pages_batch* batch, const dllm_pages_pool* pool, int32_t* lens, int32_t F,
+                    const int32_t* src, const int32_t* dst, int32_t* fresh, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Give rows[r] (no row twice) free pages until it holds those of lens[rows[r]]
+ * + extra tokens.  taken[r] = how many it took (0: it has them), -1 not served
+ * (row out of range, more than max_pages, or too few pages left, as above). */
+int dllm_pages_grow(const dllm_pages_batch* batch, const int32_t* lens, int32_t R, const int32_t* rows, int32_t extra,
+                    int32_t* taken, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Give back all pages of rows[r]: refs of each less one, held = 0 (a row given
+ * twice gives back once).  Tables keep their entries.  A page that nobody
+ * counted sets DLLM_DEVERR_PAGE and stays at 0. */
+int dllm_pages_free(const dllm_pages_batch* batch, int32_t R, const int32_t* rows, void* stream);
+
+/* Close the pool's gaps: with *used = U pages in use, those from U on move, in
+ * their order, into the free pages below U; tables (of every request) and refs
+ * follow.  map[page] = where each used page is now, -1 for a free one.  Pages
+ * that moved keep their old contents too. */
+int dllm_pages_compact(const dllm_pages_batch* batch, const dllm_pages_pool* pool, int32_t* used, int32_t* map,
+                       void* workspace, size_t workspace_bytes, void* stream);
+/* Errors of all: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_WORKSPACE, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
 
 #ifdef __cplusplus
 }
