@@ -23,6 +23,8 @@ Names follow the C ABI in ``include/dllm.h``:
 * ``page_fork`` / ``page_grow`` / ``page_free`` / ``page_copy`` /
   ``page_compact`` -- who holds which pages of a cache: shared prefixes, new
   pages, release, copies between pools, and the closing of a pool's gaps.
+* ``fp8_quantize`` / ``fp8_matmul`` -- products in 8-bit floating point with a
+  scale for each block of 128: the LM head of the masked positions.
 """
 from __future__ import annotations
 
@@ -38,6 +40,7 @@ from . import _build
 __all__ = ["load", "step", "step_host", "features", "pack_plan", "admit", "pack", "advance", "compact", "refill",
            "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict", "sample",
            "page_fork", "page_grow", "page_free", "page_copy", "page_compact",
+           "fp8_quantize", "fp8_matmul",
            "get_device_error", "DllmError", "NUM_FEATURES", "LIB_PATH"]
 
 LIB_PATH = _build.LIB_PATH
@@ -164,6 +167,17 @@ class PagesBatch(ctypes.Structure):
                 ("held", _p)]
 
 
+class Fp8QuantizeArgs(ctypes.Structure):
+    _fields_ = [("M", _i32), ("K", _i32), ("block_rows", _i32), ("pad0", _i32), ("x_rows", _i64), ("ldx", _i64), ("x", _p),
+                ("rows", _p), ("codes", _p), ("scale", _p)]
+
+
+class Fp8MatmulArgs(ctypes.Structure):
+    _fields_ = [("M", _i32), ("N", _i32), ("K", _i32), ("pad0", _i32), ("lda", _i64), ("ldb", _i64), ("ldo", _i64),
+                ("a", _p), ("a_scale", _p), ("b", _p), ("b_scale", _p), ("out", _p)]
+
+
+FP8_BLOCK = 128
 MAX_TOP = 32
 KV4_GROUP = 32
 
@@ -229,6 +243,8 @@ _SIGNATURES = {
     "dllm_kv4_attend": (ctypes.c_int, [ctypes.POINTER(Kv4AttendArgs), _p]),
     "dllm_kv4_evict": (ctypes.c_int, [ctypes.POINTER(Kv4EvictArgs), _p]),
     "dllm_sample": (ctypes.c_int, [ctypes.POINTER(SampleArgs), _p]),
+    "dllm_fp8_quantize": (ctypes.c_int, [ctypes.POINTER(Fp8QuantizeArgs), _p]),
+    "dllm_fp8_matmul": (ctypes.c_int, [ctypes.POINTER(Fp8MatmulArgs), _p]),
     "dllm_pages_workspace_size": (_sz, [_i32, _i32]),
     "dllm_pages_copy": (ctypes.c_int, [ctypes.POINTER(PagesPool), ctypes.POINTER(PagesPool), _i32, _p, _p, _p]),
     "dllm_pages_fork": (ctypes.c_int, [ctypes.POINTER(PagesBatch), ctypes.POINTER(PagesPool), _p, _i32, _p, _p, _p, _p,
@@ -273,7 +289,7 @@ def load(build=True):
             raise RuntimeError(f"libdllm ABI version {lib.dllm_abi_version()}, binding expects {ABI_VERSION}")
         for which, cls in enumerate((StepArgs, PackArgs, CompactArgs, AdvanceArgs, RefillArgs, LoopConfig, LoopInfo,
                                      VocabShard, LoopControl, LogprobsArgs, Kv4Cache, Kv4WriteArgs, Kv4AttendArgs,
-                                     Kv4EvictArgs, SampleArgs, PagesPool, PagesBatch)):
+                                     Kv4EvictArgs, SampleArgs, PagesPool, PagesBatch, Fp8QuantizeArgs, Fp8MatmulArgs)):
             if lib.dllm_struct_size(which) != ctypes.sizeof(cls):
                 raise RuntimeError(f"ABI mismatch for {cls.__name__}: library {lib.dllm_struct_size(which)} "
                                    f"bytes, binding {ctypes.sizeof(cls)}")
@@ -1213,4 +1229,74 @@ def page_compact(pools, refs, table, held):
                                 ws.data_ptr(), ws.numel(), stream)
     if rc:
         _check("dllm_pages_compact", rc)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# products in 8-bit floating point
+# ---------------------------------------------------------------------------
+def fp8_quantize(x, *, rows=None, block_rows=1):
+    """Quantise rows to 8-bit floating point with a scale for each 128 columns of
+    a row (``block_rows`` 1: activations) or of 128 rows (128: weights)
+    (dllm_fp8_quantize) on the current stream.
+
+    x:    bf16 [R, K], columns contiguous, K a multiple of 16
+    rows: int32 [M] row of x for each row of the result (outside [0, R): zeros),
+          or None: all of them
+    Returns (codes float8_e4m3fn [M, K], scale float32 [ceil(M / block_rows),
+    ceil(K / 128)])."""
+    torch = _torch()
+    dev = x.device
+    _check_tensors(torch, dev, rows)
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise TypeError("x must be bf16 [R, K]")
+    R, K = x.shape
+    ldx, kc = x.stride()
+    if kc != 1 and K > 1:
+        raise ValueError("the columns of x must be contiguous")
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1):
+        raise TypeError("rows must be int32 [M]")
+    if block_rows != 1 and block_rows != FP8_BLOCK:
+        raise ValueError("block_rows must be 1 or 128")
+    M = R if rows is None else rows.numel()
+    codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty((-(-M // block_rows), -(-K // FP8_BLOCK)), dtype=torch.float32, device=dev)
+    a = Fp8QuantizeArgs(M, K, block_rows, 0, R, max(ldx, K) if R <= 1 else ldx, x.data_ptr(),
+                        None if rows is None else rows.data_ptr(), codes.data_ptr(), scale.data_ptr())
+    rc = (_lib or load()).dllm_fp8_quantize(ctypes.byref(a), _raw_stream(torch, dev))
+    if rc:
+        _check("dllm_fp8_quantize", rc)
+    return codes, scale
+
+
+def fp8_matmul(a, a_scale, b, b_scale, *, out=None):
+    """a @ b.T of 8-bit floating point with scales (dllm_fp8_matmul) on the
+    current stream.
+
+    a, a_scale: float8_e4m3fn [M, K] and float32 [M, ceil(K / 128)]
+    b, b_scale: float8_e4m3fn [N, K] and float32 [ceil(N / 128), ceil(K / 128)]
+    out:        bf16 [M, at least N rounded up to 8], or None: a new one of that
+                width (columns from N on are 0)
+    Returns out: rows that the step, sample and token_logprobs take as logits."""
+    torch = _torch()
+    dev = a.device
+    _check_tensors(torch, dev, a, a_scale, b, b_scale, out)
+    e4m3 = torch.float8_e4m3fn
+    if a.dtype != e4m3 or b.dtype != e4m3 or a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise TypeError("a and b must be float8_e4m3fn [M, K] and [N, K]")
+    (M, K), N = a.shape, b.shape[0]
+    blocks, float32 = -(-K // FP8_BLOCK), torch.float32
+    if a_scale.dtype != float32 or a_scale.shape != (M, blocks):
+        raise TypeError(f"a_scale must be float32 [{M}, {blocks}]")
+    if b_scale.dtype != float32 or b_scale.shape != (-(-N // FP8_BLOCK), blocks):
+        raise TypeError(f"b_scale must be float32 [{-(-N // FP8_BLOCK)}, {blocks}]")
+    if out is None:
+        out = torch.empty((M, -(-N // 8) * 8), dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.dim() != 2 or out.shape[0] != M:
+        raise TypeError(f"out must be bf16 [{M}, at least {-(-N // 8) * 8}]")
+    args = Fp8MatmulArgs(M, N, K, 0, K, K, out.shape[1], a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+                         out.data_ptr())
+    rc = (_lib or load()).dllm_fp8_matmul(ctypes.byref(args), _raw_stream(torch, dev))
+    if rc:
+        _check("dllm_fp8_matmul", rc)
     return out

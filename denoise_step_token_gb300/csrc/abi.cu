@@ -112,6 +112,8 @@ extern "C" size_t dllm_struct_size(int which) {
         case 14: return sizeof(dllm_sample_args);
         case 15: return sizeof(dllm_pages_pool);
         case 16: return sizeof(dllm_pages_batch);
+        case 17: return sizeof(dllm_fp8_quantize_args);
+        case 18: return sizeof(dllm_fp8_matmul_args);
         default: return 0;
     }
 }

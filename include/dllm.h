@@ -79,7 +79,8 @@ int dllm_last_cuda_error(const char** name);
  * 6 dllm_loop_info_t, 7 dllm_vocab_shard, 8 dllm_loop_control,
  * 9 dllm_logprobs_args, 10 dllm_kv4_cache, 11 dllm_kv4_write_args,
  * 12 dllm_kv4_attend_args, 13 dllm_kv4_evict_args, 14 dllm_sample_args,
- * 15 dllm_pages_pool, 16 dllm_pages_batch.  Returns 0 for an unknown `which`. */
+ * 15 dllm_pages_pool, 16 dllm_pages_batch,
+ * 17 dllm_fp8_quantize_args, 18 dllm_fp8_matmul_args.  Returns 0 for an unknown `which`. */
 size_t dllm_struct_size(int which);
 
 /* Fault injection for tests of the status plumbing (host only; nothing
@@ -1030,6 +1031,63 @@ int dllm_pages_free(const dllm_pages_batch* batch, int32_t R, const int32_t* row
 int dllm_pages_compact(const dllm_pages_batch* batch, const dllm_pages_pool* pool, int32_t* used, int32_t* map,
                        void* workspace, size_t workspace_bytes, void* stream);
 /* Errors of all: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_WORKSPACE, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+
+/* ======================================================================
+ * Products in 8-bit floating point (e4m3: 4 exponent and 3 fraction bits,
+ * finite, largest value 448) with 32-bit scales: the LM head whose logits the
+ * step reads, for the masked positions' rows (dllm_step_compact, dllm_sample
+ * and dllm_logprobs take its output), and any other projection of a model.
+ * ====================================================================== */
+#define DLLM_FP8_BLOCK 128
+
+/* Quantise rows of bf16: row i of the result is row r of x (r = rows[i], or i
+ * when rows is NULL; a row outside [0, x_rows) counts as zeros).  A group is
+ * the 128 columns from a multiple of 128 on (the last one may be shorter), of
+ * one row (block_rows 1: activations) or of 128 rows from a multiple of 128 on
+ * (block_rows 128: weights):
+ *   scale = max(max |x| / 448, 2^-126);  code = x / scale to the nearest e4m3
+ * (both quotients rounded to 32 bits; ties to even).  A group holding an
+ * infinity or a NaN gets scale NaN and codes 0.
+ *   - K a multiple of 16, ldx of 8, x and codes 16-byte aligned.
+ * Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+typedef struct dllm_fp8_quantize_args {
+    int32_t M;                  /* rows of the result, 0..65535 * 128 */
+    int32_t K;                  /* columns, 16..2^24 */
+    int32_t block_rows;         /* 1 or DLLM_FP8_BLOCK */
+    int32_t pad0;
+    int64_t x_rows;             /* rows of x (>= 0) */
+    int64_t ldx;                /* row stride of x in elements, >= K */
+    const uint16_t* x;          /* device bf16 [x_rows][ldx] */
+    const int32_t* rows;        /* device [M], or NULL */
+    uint8_t* codes;             /* device [M][K] out */
+    float* scale;               /* device [ceil(M / block_rows)][ceil(K / 128)] out */
+} dllm_fp8_quantize_args;
+
+int dllm_fp8_quantize(const dllm_fp8_quantize_args* args, void* stream);
+
+/* out[m][n] = sum_g a_scale[m][g] b_scale[n / 128][g] sum_{k in group g}
+ * a[m][k] b[n][k], g the groups of 128 columns, rounded to bf16 once.  The
+ * inner sums and the outer one are held in 32 bits, groups in ascending order:
+ * an output depends on its two rows alone, and equal calls give equal bits.
+ * Columns N up to the next multiple of 8 receive 0.
+ *   - K, lda and ldb multiples of 16, ldo of 8 and at least N rounded up to 8;
+ *     a, b and out 16-byte aligned.
+ * Serves inference: no gradient.  Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN,
+ * DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
+typedef struct dllm_fp8_matmul_args {
+    int32_t M, N;               /* rows of a (>= 0) and of b (>= 1), up to 2^28 */
+    int32_t K;                  /* 16..2^24 */
+    int32_t pad0;
+    int64_t lda, ldb;           /* row strides in bytes, >= K */
+    int64_t ldo;                /* row stride of out in elements */
+    const uint8_t* a;           /* device e4m3 [M][lda] */
+    const float* a_scale;       /* device [M][ceil(K / 128)] */
+    const uint8_t* b;           /* device e4m3 [N][ldb] */
+    const float* b_scale;       /* device [ceil(N / 128)][ceil(K / 128)] */
+    uint16_t* out;              /* device bf16 [M][ldo] */
+} dllm_fp8_matmul_args;
+
+int dllm_fp8_matmul(const dllm_fp8_matmul_args* args, void* stream);
 
 #ifdef __cplusplus
 }
