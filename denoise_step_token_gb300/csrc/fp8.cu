@@ -136,13 +136,19 @@ constexpr int kRows = 128;                      // of A, and of B, that a CTA ho
 constexpr int kTile = 2 * kRows;                // the pair's tile is kTile x kTile
 constexpr int kStages = 6;
 constexpr uint32_t kOperand = kRows * kBlock;   // bytes of one operand's part of a stage
-constexpr int kSumWarps = 8, kCopyWarp = 8, kIssueWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kSumWarps = 16, kCopyWarp = kSumWarps, kIssueWarp = kSumWarps + 1;
+constexpr int kCols = kTile / (kSumWarps / 4);   // columns of a thread
+constexpr int kThreads = (kSumWarps + 4) * 32;   // the last two warps only fill the warpgroup
+// Registers per thread: 96 at launch (640 threads); the last warpgroup gives 32 each to the four that hold sums:
+// 128 (96 - 64) >= 512 (104 - 96).  With 96 for all, the sums spill (1117 us for 996, 1851 x 151936 x 3584).
+constexpr int kLaunchRegs = 96, kSumRegs = 104, kOtherRegs = 64;
+static_assert(128 * (kLaunchRegs - kOtherRegs) >= kSumWarps * 32 * (kSumRegs - kLaunchRegs), "registers given cover those taken");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct MatmulParams {
     CUtensorMap a, b;
     int M, N, blocks, m_tiles;
+    int wide;   // rows of out lie on 32-byte boundaries
     long long tiles;
     long long ldo;
     const float* a_scale;
@@ -200,7 +206,7 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint32_t b, uin
 
 // A wait that gives up (and with it every later one of the CTA).
 __device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, Shared& sh, int* err) {
-    if (*(volatile int*)&sh.abort) return;
+    if (mbar_test_wait(bar, parity) || *(volatile int*)&sh.abort) return;
     if (mbar_wait_bounded(bar, parity, kWaitNs)) return;
     set_error(err, DLLM_DEVERR_TIMEOUT);
     *(volatile int*)&sh.abort = 1;
@@ -238,7 +244,77 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_matmul_kernel(const __grid_co
     pdl_wait();
     pdl_release();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    if (warp == kCopyWarp) {
+    if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < kSumWarps) {
+        // ---------------------------------------------------------- sums: a thread a row and kCols columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        const int part = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's quarter of TMEM's lanes
+        uint32_t n = 0;
+        for (long long t = pair; t < P.tiles; t += pairs) {
+            const int m = (int)(t % P.m_tiles) * kTile + rank * kRows + (warp & 3) * 32 + lane;
+            const int n0 = (int)(t / P.m_tiles) * kTile + part * kCols;
+            const float* const sa = P.a_scale + (long long)min(m, P.M - 1) * P.blocks;
+            const float* const sb = P.b_scale + (long long)min(n0 / kBlock, (P.N - 1) / kBlock) * P.blocks;
+            unsigned long long acc[kCols / 2];
+#pragma unroll
+            for (int c = 0; c < kCols / 2; ++c) acc[c] = 0;
+            float sa_next = __ldg(sa), sb_next = __ldg(sb);
+            for (int b = 0; b < P.blocks; ++b, ++n) {
+                const uint32_t buf = n & 1;
+                const unsigned long long s2 = f32x2_splat(sa_next * sb_next);
+                if (b + 1 < P.blocks) {
+                    sa_next = __ldg(sa + b + 1);
+                    sb_next = __ldg(sb + b + 1);
+                }
+                wait_for(smem_addr(&sh.ready[buf]), n >> 1 & 1, sh, P.err);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t from = tmem + lanes + buf * kTile + part * kCols;
+#pragma unroll
+                for (int c0 = 0; c0 < kCols; c0 += 16) {
+                    uint32_t v[16];
+                    tc_ld16(v, from + c0);
+                    tc_wait_ld();
+                    if (c0 + 16 == kCols) {   // all read: the next block but one may be formed
+                        tc_fence_before();
+                        __syncwarp();
+                        // (released at CTA scope: no memory but TMEM is handed over, and a cluster-wide release costs
+                        // 1500 cycles)
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_leader(smem_addr(&sh.read[buf])))
+                                         : "memory");
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        acc[c0 / 2 + c] = f32x2_fma(f32x2_pack(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), s2,
+                                                    acc[c0 / 2 + c]);
+                }
+            }
+            if (m < P.M) {
+                uint16_t* const row = P.out + (long long)m * P.ldo + n0;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    if (n0 + c >= P.N) break;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float lo = n0 + c + 2 * k < P.N ? f32x2_lo(acc[c / 2 + k]) : 0.0f;
+                        const float hi = n0 + c + 2 * k + 1 < P.N ? f32x2_hi(acc[c / 2 + k]) : 0.0f;
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(hi), "f"(lo));
+                    }
+                    if (P.wide && n0 + c + 8 < P.N) {   // whole 32-byte sectors
+                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + c), "r"(w[0]), "r"(w[1]),
+                                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                     : "memory");
+                    } else {
+                        *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (n0 + c + 8 < P.N) *reinterpret_cast<uint4*>(row + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+            }
+        }
+    } else if (warp == kCopyWarp) {
         if (lane == 0) {
             uint32_t n = 0;
             for (long long t = pair; t < P.tiles; t += pairs) {
@@ -275,63 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_matmul_kernel(const __grid_co
                     pair_commit(smem_addr(&sh.empty[s]));
                     pair_commit(smem_addr(&sh.ready[buf]));
                 }
-        }
-    } else {
-        // ---------------------------------------------------------- sums: a thread a row and half of the columns
-        const int half = warp >> 2;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's quarter of TMEM's lanes
-        uint32_t n = 0;
-        for (long long t = pair; t < P.tiles; t += pairs) {
-            const int m = (int)(t % P.m_tiles) * kTile + rank * kRows + (warp & 3) * 32 + lane;
-            const int n0 = (int)(t / P.m_tiles) * kTile + half * kRows;
-            const float* const sa = P.a_scale + (long long)min(m, P.M - 1) * P.blocks;
-            const float* const sb = P.b_scale + (long long)min(n0 / kBlock, (P.N - 1) / kBlock) * P.blocks;
-            unsigned long long acc[kRows / 2];
-#pragma unroll
-            for (int c = 0; c < kRows / 2; ++c) acc[c] = 0;
-            float sa_next = __ldg(sa), sb_next = __ldg(sb);
-            for (int b = 0; b < P.blocks; ++b, ++n) {
-                const uint32_t buf = n & 1;
-                const unsigned long long s2 = f32x2_splat(sa_next * sb_next);
-                if (b + 1 < P.blocks) {
-                    sa_next = __ldg(sa + b + 1);
-                    sb_next = __ldg(sb + b + 1);
-                }
-                wait_for(smem_addr(&sh.ready[buf]), n >> 1 & 1, sh, P.err);
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int c0 = 0; c0 < kRows; c0 += 16) {
-                    uint32_t v[16];
-                    tc_ld16(v, tmem + lanes + buf * kTile + half * kRows + c0);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        acc[c0 / 2 + c] = f32x2_fma(f32x2_pack(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), s2,
-                                                    acc[c0 / 2 + c]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                     of_leader(smem_addr(&sh.read[buf])))
-                                 : "memory");
-            }
-            if (m < P.M) {
-                uint16_t* const row = P.out + (long long)m * P.ldo + n0;
-#pragma unroll
-                for (int c = 0; c < kRows; c += 8) {
-                    if (n0 + c >= P.N) break;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float lo = n0 + c + 2 * k < P.N ? f32x2_lo(acc[c / 2 + k]) : 0.0f;
-                        const float hi = n0 + c + 2 * k + 1 < P.N ? f32x2_hi(acc[c / 2 + k]) : 0.0f;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(hi), "f"(lo));
-                    }
-                    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
         }
     }
     // after a wait that gave up: copies still in flight land before the CTA's memory is another's
@@ -433,11 +452,20 @@ extern "C" int dllm_fp8_matmul(const dllm_fp8_matmul_args* a, void* stream) {
     P.m_tiles = (a->M + kTile - 1) / kTile;
     P.tiles = (long long)P.m_tiles * ((a->N + kTile - 1) / kTile);
     P.ldo = a->ldo;
+    P.wide = a->ldo % 16 == 0 && (reinterpret_cast<uintptr_t>(a->out) & 31) == 0;
     P.a_scale = a->a_scale;
     P.b_scale = a->b_scale;
     P.out = a->out;
     static SmemOnce done;
     DLLM_CUDA_TRY(allow_smem(fp8_matmul_kernel, kSmem, done));
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_acquire) == 0) {
+        cudaFuncAttributes attr;
+        DLLM_CUDA_TRY(cudaFuncGetAttributes(&attr, fp8_matmul_kernel));
+        regs.store(attr.numRegs, std::memory_order_release);
+    }
+    // the split of registers above is of kLaunchRegs: with fewer at launch the sums' warps would wait for ever
+    if (regs.load(std::memory_order_acquire) != kLaunchRegs) return DLLM_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<long long>(P.tiles, sms / 2) * 2);
     cfg.blockDim = dim3(kThreads);
