@@ -19,7 +19,8 @@ Names follow the C ABI in ``include/dllm.h``:
 * ``kv4_pages`` / ``kv4_write`` / ``kv4_attend`` / ``kv4_evict`` -- the paged
   cache of keys and values in 4 bits: its pool, the write, a block's
   attention over it, and its thinning by attention weight.
-* ``sample`` -- tokens drawn from the step's logits by given random numbers.
+* ``sample`` / ``step_sampled`` -- tokens drawn from the step's logits by given
+  random numbers, and the step that commits them.
 * ``page_fork`` / ``page_grow`` / ``page_free`` / ``page_copy`` /
   ``page_compact`` -- who holds which pages of a cache: shared prefixes, new
   pages, release, copies between pools, and the closing of a pool's gaps.
@@ -38,7 +39,7 @@ import numpy as np
 from . import _build
 
 __all__ = ["load", "step", "step_host", "features", "pack_plan", "admit", "pack", "advance", "compact", "refill",
-           "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict", "sample",
+           "token_logprobs", "kv4_pages", "kv4_write", "kv4_attend", "kv4_evict", "sample", "step_sampled",
            "page_fork", "page_grow", "page_free", "page_copy", "page_compact",
            "fp8_quantize", "fp8_matmul",
            "get_device_error", "DllmError", "NUM_FEATURES", "LIB_PATH"]
@@ -1080,6 +1081,49 @@ def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=
     rc = (_lib or load()).dllm_sample(ctypes.byref(a), _raw_stream(torch, dev))
     if rc:
         _check("dllm_sample", rc)
+    return out
+
+
+def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=True, debug=False, quota=None):
+    """The denoise step with drawn tokens (``sample``) in place of the argmax:
+    selection by the probability of each draw, update, done and features as in
+    ``step`` (dllm_step_merge over one shard).
+
+    tokens, prob: int32 and float32 [B * L], read at the masked positions (the
+                  others' rows may be skipped: -1 in ``sample``'s rows).  A
+                  masked position without a token counts as confidence 0.
+    The other arguments and the outputs are those of ``step``; conf is the
+    draw's probability."""
+    torch = _torch()
+    dev = _require_cuda(tokens, prob, input_ids, conf_state, thr, quota)
+    B, L = input_ids.shape
+    if tokens.dtype != torch.int32 or prob.dtype != torch.float32 or tokens.numel() != B * L or prob.numel() != B * L:
+        raise TypeError("tokens int32 and prob float32 of one entry per position expected")
+    if input_ids.dtype != torch.int32 or conf_state.dtype != torch.float32:
+        raise TypeError("input_ids int32, conf_state float32 expected")
+    if quota is None and thr is None:
+        raise ValueError("thr or quota expected")
+    for name, t, dtype in (("thr", thr, torch.float32), ("quota", quota, torch.int32)):
+        if t is not None and (t.dtype != dtype or t.numel() != B):
+            raise TypeError(f"{name} must be {dtype} [{B}]")
+    m = torch.zeros(B * L, dtype=torch.float32, device=dev)
+    s = torch.where(prob > 0, 1.0 / prob, float("inf"))
+    out = {"done": torch.empty(B, dtype=torch.uint8, device=dev),
+           "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
+           "n_new": torch.empty(B, dtype=torch.int32, device=dev)}
+    if feats:
+        out["feats"] = torch.empty((B, NUM_FEATURES), dtype=torch.float32, device=dev)
+    if debug:
+        out["conf"] = torch.full((B, L), float("nan"), dtype=torch.float32, device=dev)
+        out["tok"] = torch.full((B, L), -1, dtype=torch.int32, device=dev)
+    lib = load()
+    ws = _step_ws.get(dev, int(lib.dllm_step_workspace_size(B, L, V)))
+    a = StepArgs(B=B, L=L, V=V, mask_id=mask_id, ldv=-(-V // 8) * 8, logits=None, input_ids=_ptr(input_ids), thr=_ptr(thr),
+                 conf_state=_ptr(conf_state), done=_ptr(out["done"]), accept_len=_ptr(out["accept_len"]),
+                 n_new=_ptr(out["n_new"]), feats=_ptr(out.get("feats")), conf_out=_ptr(out.get("conf")), lse_out=None,
+                 tok_out=_ptr(out.get("tok")), workspace=_ptr(ws), workspace_bytes=ws.numel())
+    _check("dllm_step_merge", lib.dllm_step_merge(ctypes.byref(a), 1, _ptr(m), _ptr(s), _ptr(tokens), B * L, _ptr(quota),
+                                                  _stream(dev)))
     return out
 
 

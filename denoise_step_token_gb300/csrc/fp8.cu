@@ -433,7 +433,7 @@ extern "C" int dllm_fp8_matmul(const dllm_fp8_matmul_args* a, void* stream) {
         return DLLM_ERR_INVAL;
     if (a->M > 0 && (!a->a || !a->b || !a->a_scale || !a->b_scale || !a->out)) return DLLM_ERR_INVAL;
     const uintptr_t all = reinterpret_cast<uintptr_t>(a->a) | reinterpret_cast<uintptr_t>(a->b) | reinterpret_cast<uintptr_t>(a->out);
-    if ((all & 15) || a->lda % 16 || a->ldb % 16 || a->ldo % 8) return DLLM_ERR_ALIGN;
+    if ((all & 15) || a->K % 16 || a->lda % 16 || a->ldb % 16 || a->ldo % 8) return DLLM_ERR_ALIGN;
     if (a->K > 1 << 24 || a->M > 1 << 28 || a->N > 1 << 28 || a->lda > 1ll << 38 || a->ldb > 1ll << 38)
         return DLLM_ERR_UNSUPPORTED;
     if (a->M == 0) return DLLM_OK;
