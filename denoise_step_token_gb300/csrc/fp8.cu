@@ -9,14 +9,19 @@
 //
 // Tile: 256 x 256 by a pair of CTAs (cta_group::2): each holds 128 rows of A and
 // 128 of B, and the 128 x 256 sums of its own rows.  A block of 128 is 4 products
-// of 512 cycles together; meanwhile 8 warps a CTA read 128 x 256 sums (a thread a
-// row and 128 columns) and spend 64 packed operations a thread on them.  What the
-// pair saves is L2 traffic: 32 KB a CTA and block, 64 bytes a cycle; single CTAs
-// with 128 x 256 tiles would need 96.
+// of 512 cycles together; meanwhile 16 warps a CTA read 128 x 256 sums (a thread a
+// row and 64 columns) and add them with 32 packed operations a thread.  What the
+// pair saves is L2 traffic: 32 KB a CTA and block; single CTAs with 128 x 256 tiles
+// would need 48.
+// What bounds it: those sums, about 1000 cycles a block with the barriers on both
+// sides (tensor pipes 53 % active).  1851 x 151936 x 3584: 887 us, 2270 TFLOP/s; 21 x
+// 126464 x 4096: 143 us, 3.6 TB/s of weights.  With 8 warps of sums and 128 columns a
+// thread 1037 and 187 us.
 // Two TMEM buffers of 256 columns: a block's sums are read while the next block's
 // are formed.  Six stages of 32 KB in shared memory.
 // Tiles run along the rows of A first: the CTAs in flight share few tiles of B, which
-// comes from DRAM once, and A stays in L2.
+// comes from DRAM once, and A stays in L2.  For few rows the tile is the same: its
+// products cost less than reading the weights.
 #include <cuda.h>
 #include <math.h>
 #include <stdint.h>
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_matmul_kernel(const __grid_co
                         const float hi = n0 + c + 2 * k + 1 < P.N ? f32x2_hi(acc[c / 2 + k]) : 0.0f;
                         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(hi), "f"(lo));
                     }
-                    if (P.wide && n0 + c + 8 < P.N) {   // whole 32-byte sectors
+                    if (P.wide && n0 + c + 8 < P.N) {   // whole 32-byte sectors (halves of them: 1010 us for 887)
                         asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + c), "r"(w[0]), "r"(w[1]),
                                      "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                                      : "memory");

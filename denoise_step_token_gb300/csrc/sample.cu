@@ -18,7 +18,12 @@
 // warps count values with shared-memory atomics.  Segments of 32 values are
 // summed by all warps of the cluster (counts of the others by distributed shared
 // memory), one warp walks the segments' sums, and the CTA whose slice holds the
-// token reads its slice again (from L2) to find it.
+// token reads its slice again, from its end, to find it.
+// What bounds it: the phases of a row follow one another, two CTAs an SM overlap; issue
+// slots are 57 % used, much of it the counters' shared-memory atomics.  1851 rows of
+// 151936 values: 282 us (2.0 TB/s; without the atomics 123, without the search 238).
+// CTAs a row: as many as fill the SMs, none with under 4096 values.  More than
+// needed cost: 353 us for clusters of two in that batch.
 #include <math.h>
 #include <stdint.h>
 
