@@ -1305,7 +1305,7 @@ def fp8_quantize(x, *, rows=None, block_rows=1):
     M = R if rows is None else rows.numel()
     codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     scale = torch.empty((-(-M // block_rows), -(-K // FP8_BLOCK)), dtype=torch.float32, device=dev)
-    a = Fp8QuantizeArgs(M, K, block_rows, 0, R, max(ldx, K) if R <= 1 else ldx, x.data_ptr(),
+    a = Fp8QuantizeArgs(M, K, block_rows, 0, R, K if R <= 1 else ldx, x.data_ptr(),
                         None if rows is None else rows.data_ptr(), codes.data_ptr(), scale.data_ptr())
     rc = (_lib or load()).dllm_fp8_quantize(ctypes.byref(a), _raw_stream(torch, dev))
     if rc:

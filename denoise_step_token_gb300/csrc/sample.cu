@@ -744,6 +744,8 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
                 }
             }
         }
+        __syncwarp();
+        if (ctas > 1) cluster_sync();
         return;
     }
     // ------------------------------------------------------------------ counts
@@ -939,7 +941,8 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
             bits = peer_load(at + offsetof(Found, bits), 0);
             r = peer_load(at + offsetof(Found, r), 0);
             mine = false;
-            const uint32_t counter = (bits & 0x8000u ? kNegative : 0u) + ((bits & 0x7fffu) == 0 ? 0 : ((bits & 0x7fffu) - kLow) * 4);
+            const uint32_t c0 = (bits & 0x7fffu) == 0 ? 0 : min((bits & 0x7fffu) - kLow, (uint32_t)kValues);
+            const uint32_t counter = (bits & 0x8000u ? kNegative : 0u) + c0 * 4;
 #pragma unroll 1
             for (int q = 0; q <= rank; ++q) {
                 const uint32_t c = peer_load(base + counter, q);
@@ -959,6 +962,9 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
     }
     // after a wait that gave up: copies still in flight land in this CTA's memory, not in its successor's
     if (*(volatile int*)&sh.abort) __nanosleep(1000000);
+    // no CTA leaves while another may arrive at its barriers, even where waits gave up
+    __syncwarp();
+    if (ctas > 1) cluster_sync();
 }
 
 }  // namespace

@@ -87,6 +87,16 @@ def test_quantize_every_value(dllm, block_rows):
     same(scale, want[1])
 
 
+def test_quantize_one_row_of_any_stride(dllm):
+    """A single row's stride says nothing; its address does."""
+    import torch
+    x = torch.randn(1, 131).to(torch.bfloat16)
+    codes, scale = dllm.fp8_quantize(x.to(dev())[:, :128])
+    want = quantised(x[:, :128].float(), 1)
+    same(codes, want[0])
+    same(scale, want[1])
+
+
 def made(gen, M, N, K):
     import torch
     a = torch.randn(M, K, generator=gen) * torch.exp(torch.randn(1, K, generator=gen))
