@@ -21,7 +21,8 @@
 // token reads its slice again, from its end, to find it.
 // What bounds it: the phases of a row follow one another, two CTAs an SM overlap; issue
 // slots are 57 % used, much of it the counters' shared-memory atomics.  1851 rows of
-// 151936 values: 282 us (2.0 TB/s; without the atomics 123, without the search 238).
+// 151936 values: 270 us (2.1 TB/s; on the way there, at 292: without the search 238, without the
+// counters' atomics too 123).
 // CTAs a row: as many as fill the SMs, none with under 4096 values.  More than
 // needed cost: 353 us for clusters of two in that batch.
 #include <math.h>
@@ -36,10 +37,12 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 512;   // counting threads of a CTA (256: 320 us instead of 292, 1851 rows of 151936)
+constexpr int kThreads = 512;   // counting threads of a CTA (256: 320 us instead of 292 on the way, 1851 rows of 151936)
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 7;
-constexpr int kChunk = 4096;    // values of a stage
+// The ring: fewer, larger copies leave fewer barriers a value (7 stages of 4096 values: 285 us instead of 270).
+constexpr int kStages = 3;
+constexpr int kChunk = 8192;    // values of a stage
+constexpr int kLeast = 4096;    // values of the smallest slice worth a CTA
 constexpr int kPerSm = 2;
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -997,7 +1000,7 @@ extern "C" int dllm_sample(const dllm_sample_args* a, void* stream) {
     P.err = error_word_ptr();
     if (!P.err) return DLLM_ERR_CUDA;
     int c = 1;
-    while (c < kMaxCluster && (long long)a->N * c < sms && a->V / (2 * c) >= kChunk) c *= 2;
+    while (c < kMaxCluster && (long long)a->N * c < sms && a->V / (2 * c) >= kLeast) c *= 2;
     P.cluster = c;
     P.slice = ((a->V + c - 1) / c + 7) / 8 * 8;
     int bits = 0;   // V tokens of mass 2^(62 - shift) stay below 2^62
