@@ -197,3 +197,41 @@ def test_equal_calls_batches_and_graphs(dllm):
     torch.cuda.synchronize()
     assert torch.equal(out["tokens"], whole["tokens"])
     assert dllm.get_device_error(dev) == 0
+
+
+def test_calls_at_once(dllm):
+    """Calls of one row (a cluster of CTAs) and of many, on streams of their own and in graphs replayed side by side, and
+    products between them: everyone gets its own draws."""
+    import torch
+    dev = torch.device("cuda", 0)
+    rng = np.random.default_rng(6)
+    work = []
+    for n, V in ((1, 126464), (3, 40000), (200, 9000), (37, 32003)):
+        x = torch.from_numpy(rows(rng, n, V, "plain")).to(torch.bfloat16).to(dev)
+        x = torch.nn.functional.pad(x, (0, -V % 8)).contiguous()
+        work.append((x, torch.rand(n, device=dev), V))
+    want = [dllm.sample(x, u, V=V) for x, u, V in work]
+    a, sa = dllm.fp8_quantize(torch.randn(300, 512, device=dev).to(torch.bfloat16))
+    b, sb = dllm.fp8_quantize(torch.randn(2000, 512, device=dev).to(torch.bfloat16), block_rows=128)
+    product = dllm.fp8_matmul(a, sa, b, sb)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, u, V in work:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((dllm.sample(x, u, V=V), dllm.fp8_matmul(a, sa, b, sb)))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for k, (x, u, V) in enumerate(work):
+            with torch.cuda.stream(streams[k]):
+                got.append((k, dllm.sample(x, u, V=V)))
+            with torch.cuda.stream(streams[4 + k]):
+                graphs[k].replay()
+    torch.cuda.synchronize()
+    for k, o in got + [(k, o[0]) for k, o in enumerate(outs)]:
+        assert torch.equal(o["tokens"], want[k]["tokens"]) and torch.equal(o["prob"], want[k]["prob"])
+    assert all(torch.equal(o[1], product) for o in outs)
+    assert dllm.get_device_error(dev) == 0
