@@ -781,8 +781,10 @@ class _StreamWorkspace:
 WORKSPACE_ZEROED = 8192   # include/dllm.h DLLM_WORKSPACE_ZEROED
 
 
-def _call(torch, fn, args, dev, stream, nbytes, workspace):
-    """fn(args, stream) with the caller's workspace, or the stream's own.
+def _call(torch, fn, args, dev, stream, nbytes, workspace, kept=_stream_ws, zeroed=WORKSPACE_ZEROED):
+    """fn(args, stream) with the caller's workspace, or the stream's own out of
+    ``kept`` (operators that need different bytes at zero between calls keep
+    theirs apart; the first ``zeroed`` have to be).
 
     A call that is being captured into a CUDA graph gets memory of the graph's
     pool, cleared in the graph where it must be: replays then depend on no
@@ -793,12 +795,12 @@ def _call(torch, fn, args, dev, stream, nbytes, workspace):
         args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
         return fn(ctypes.byref(args), stream)
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(nbytes, WORKSPACE_ZEROED), dtype=torch.uint8, device=dev)
-        ws[:WORKSPACE_ZEROED].zero_()
+        ws = torch.empty(max(nbytes, zeroed), dtype=torch.uint8, device=dev)
+        ws[:zeroed].zero_()
         args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
         return fn(ctypes.byref(args), stream)
     key = (dev.index, stream)
-    own = _stream_ws.get(key) or _stream_ws.setdefault(key, _StreamWorkspace())
+    own = kept.get(key) or kept.setdefault(key, _StreamWorkspace())
     with own.lock:
         ws = own.buf
         if ws is None or ws.numel() < nbytes:
@@ -1084,7 +1086,11 @@ def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=
     return out
 
 
-def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=True, debug=False, quota=None):
+_drawn_ws = {}   # step_sampled's workspaces, a step's whole zero between calls
+
+
+def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=True, debug=False, quota=None,
+                 workspace=None):
     """The denoise step with drawn tokens (``sample``) in place of the argmax:
     selection by the probability of each draw, update, done and features as in
     ``step`` (dllm_step_merge over one shard).
@@ -1092,6 +1098,9 @@ def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=
     tokens, prob: int32 and float32 [B * L], read at the masked positions (the
                   others' rows may be skipped: -1 in ``sample``'s rows).  A
                   masked position without a token counts as confidence 0.
+    workspace:    as ``step``'s, for (B, L, V); default: one kept for the
+                  current stream (while a CUDA graph is captured: one of the
+                  graph's own, cleared in it)
     The other arguments and the outputs are those of ``step``; conf is the
     draw's probability."""
     torch = _torch()
@@ -1117,13 +1126,15 @@ def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=
         out["conf"] = torch.full((B, L), float("nan"), dtype=torch.float32, device=dev)
         out["tok"] = torch.full((B, L), -1, dtype=torch.int32, device=dev)
     lib = load()
-    ws = _step_ws.get(dev, int(lib.dllm_step_workspace_size(B, L, V)))
     a = StepArgs(B=B, L=L, V=V, mask_id=mask_id, ldv=-(-V // 8) * 8, logits=None, input_ids=_ptr(input_ids), thr=_ptr(thr),
                  conf_state=_ptr(conf_state), done=_ptr(out["done"]), accept_len=_ptr(out["accept_len"]),
                  n_new=_ptr(out["n_new"]), feats=_ptr(out.get("feats")), conf_out=_ptr(out.get("conf")), lse_out=None,
-                 tok_out=_ptr(out.get("tok")), workspace=_ptr(ws), workspace_bytes=ws.numel())
-    _check("dllm_step_merge", lib.dllm_step_merge(ctypes.byref(a), 1, _ptr(m), _ptr(s), _ptr(tokens), B * L, _ptr(quota),
-                                                  _stream(dev)))
+                 tok_out=_ptr(out.get("tok")))
+    # the merge takes a workspace for any V: its own is for the least
+    need = int(lib.dllm_step_workspace_size(B, L, 1))
+    _check("dllm_step_merge", _call(torch, lambda args, stream: lib.dllm_step_merge(
+        args, 1, _ptr(m), _ptr(s), _ptr(tokens), B * L, _ptr(quota), stream), a, dev, _raw_stream(torch, dev), need,
+        workspace, _drawn_ws, need))
     return out
 
 

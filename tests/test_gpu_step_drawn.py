@@ -1,0 +1,84 @@
+"""step_sampled: the step over given tokens and confidences, where tokens are missing, confidences lie on a threshold,
+and calls run side by side."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def dev():
+    import torch
+    return torch.device("cuda", 0)
+
+
+def test_calls_at_once(dllm):
+    """Batches of several shapes on streams of their own, beside plain steps and replayed graphs, one of which was captured
+    before any other call of its size: everyone gets its own results."""
+    import torch
+    rng = np.random.default_rng(2)
+    d = dev()
+    work = []
+    for B, L, V in ((300, 32, 500), (7, 700, 2000), (64, 100, 1000), (1, 1, 9)):
+        ids = torch.from_numpy(np.where(rng.random((B, L)) < 0.7, V, 3).astype(np.int32)).to(d)
+        tok = torch.from_numpy(rng.integers(0, V, B * L).astype(np.int32)).to(d)
+        conf = torch.from_numpy(rng.random(B * L).astype(np.float32) * 0.9 + 0.1).to(d)
+        thr = torch.from_numpy(rng.random(B).astype(np.float32)).to(d)
+        work.append((ids, tok, conf, thr, V))
+
+    def turn(w):
+        ids, tok, conf, thr, V = w
+        thr = thr[:len(ids)]
+        mine, cs = ids.clone(), torch.full(ids.shape, float("nan"), device=d)
+        out = dllm.step_sampled(tok, conf, mine, thr, cs, V=V, mask_id=V, debug=True)
+        return [mine, cs, *(out[k] for k in sorted(out))]
+
+    turn([t[:1] if k < 1 else t[:32] if k < 3 else t for k, t in enumerate(work[0])])   # loads the kernels: not while capturing
+    graphs, replayed = [], []
+    for w in work:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            replayed.append(turn(w))
+        graphs.append(g)
+    want = [turn(w) for w in work]
+    B, L, V = 64, 32, 4000
+    logits = torch.from_numpy(rng.standard_normal((B * L, V)) * 3).to(torch.bfloat16).to(d)
+    blocks = torch.full((B, L), V, dtype=torch.int32, device=d)
+    thr = torch.full((B,), 0.3, device=d)
+
+    def plain():
+        ids, cs = blocks.clone(), torch.full((B, L), float("nan"), device=d)
+        return ids, cs, dllm.step(logits, ids, thr, cs, V=V, mask_id=V)["n_new"]
+    plain_want = plain()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    got, steps = [], []
+    for _ in range(10):
+        for k, w in enumerate(work):
+            with torch.cuda.stream(streams[k]):
+                got.append((k, turn(w)))
+            with torch.cuda.stream(streams[4 + k]):
+                graphs[k].replay()
+        steps.append(plain())
+    torch.cuda.synchronize()
+    same = lambda a, b: all(x.equal(y) or torch.equal(x.nan_to_num(-5), y.nan_to_num(-5)) for x, y in zip(a, b))  # noqa: E731
+    for k, o in got + list(enumerate(replayed)):
+        assert same(o, want[k])
+    assert all(same(o, plain_want) for o in steps)
+    assert dllm.get_device_error(d) == 0
+
+
+def test_a_caller_s_workspace(dllm):
+    import torch
+    d = dev()
+    ids = torch.full((3, 8), 50, dtype=torch.int32, device=d)
+    tok, conf = torch.arange(24, dtype=torch.int32, device=d), torch.linspace(0.1, 0.9, 24, device=d)
+    thr, cs = torch.full((3,), 0.5, device=d), torch.zeros(3, 8, device=d)
+    ws = torch.zeros(dllm.step_workspace_size(3, 8, 50), dtype=torch.uint8, device=d)
+    out = dllm.step_sampled(tok, conf, ids, thr, cs, V=50, mask_id=50, workspace=ws)
+    assert out["n_new"].tolist() == [1, 4, 8] and out["done"].tolist() == [0, 0, 1]
+    for bad in (ws[:100], ws[1:]):
+        with pytest.raises(dllm.DllmError):
+            dllm.step_sampled(tok, conf, ids, thr, cs, V=50, mask_id=50, workspace=bad)
+    with pytest.raises(ValueError):
+        dllm.step_sampled(tok, conf, ids, thr, cs, V=50, mask_id=50, workspace=ws.cpu())
+    assert dllm.get_device_error(d) == 0

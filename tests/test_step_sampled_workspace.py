@@ -1,0 +1,78 @@
+"""The default workspace of step_sampled, on the CPU: which memory a call gets, and who else may be using it.
+
+The library is replaced by one that records the workspace each call is given, and the checks that ask for a CUDA device
+are taken out."""
+import ctypes
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import denoise_step_token_gb300 as pkg
+
+NEED = 20000
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    state = SimpleNamespace(given=[], stream=7, capturing=False)
+
+    def call(ref, *rest):
+        args = ref._obj
+        raw = (ctypes.c_uint8 * args.workspace_bytes).from_address(args.workspace)
+        state.given.append((args.workspace, args.workspace_bytes, not any(raw[:NEED])))
+        return 0
+
+    lib = SimpleNamespace(dllm_step_merge=call, dllm_step_drawn=call, dllm_step_workspace_size=lambda *a: NEED)
+    monkeypatch.setattr(pkg, "_lib", lib)
+    monkeypatch.setattr(pkg, "_require_cuda", lambda *a: torch.device("cpu"))
+    monkeypatch.setattr(pkg, "_check_tensors", lambda *a: None)
+    monkeypatch.setattr(pkg, "_raw_stream", lambda *a: state.stream)
+    monkeypatch.setattr(pkg, "_stream", lambda *a: ctypes.c_void_p(state.stream))
+    monkeypatch.setattr(pkg, "_step_ws", pkg._Workspaces())
+    monkeypatch.setattr(pkg, "_stream_ws", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
+    monkeypatch.setattr(pkg, "_drawn_ws", {})
+    return state
+
+
+def step(**kw):
+    B, L = 2, 4
+    return pkg.step_sampled(torch.zeros(B * L, dtype=torch.int32), torch.ones(B * L), torch.zeros(B, L, dtype=torch.int32),
+                            torch.zeros(B), torch.zeros(B, L), V=50, mask_id=50, **kw)
+
+
+def test_every_stream_has_its_own(fake):
+    step()
+    step()
+    fake.stream = 8
+    step()
+    (a, n, zero), (b, *_), (c, _, clear) = fake.given
+    assert a == b != c and n >= NEED and zero and clear
+
+
+def test_none_of_it_is_the_step_s(fake):
+    step()
+    assert fake.given[0][0] != pkg._step_ws.get(torch.device("cpu"), NEED).data_ptr()
+    assert not pkg._stream_ws                      # nor that of the operators that clear their counters alone
+
+
+def test_a_graph_has_its_own_cleared(fake, monkeypatch):
+    empty, held = torch.empty, []   # kept, so that addresses are not used again; as dirty as memory may be
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: held.append(empty(*a, **k).fill_(1)) or held[-1])
+    fake.capturing = True
+    step()
+    fake.capturing = False
+    step()
+    (a, n, zero), (b, *_) = fake.given
+    assert a != b and zero and n >= NEED
+    assert [w.buf.data_ptr() for w in pkg._drawn_ws.values()] == [b]
+
+
+def test_a_caller_s_own(fake):
+    own = torch.zeros(30000, dtype=torch.uint8)
+    step(workspace=own)
+    assert fake.given[0][:2] == (own.data_ptr(), 30000) and not pkg._drawn_ws
+    for bad in (own.int(), own[::2]):
+        with pytest.raises(ValueError):
+            step(workspace=bad)
