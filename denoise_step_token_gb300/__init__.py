@@ -1097,7 +1097,8 @@ def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=
 
     tokens, prob: int32 and float32 [B * L], read at the masked positions (the
                   others' rows may be skipped: -1 in ``sample``'s rows).  A
-                  masked position without a token counts as confidence 0.
+                  masked position without a token (-1) stays masked and counts
+                  in neither rule: a block that lacks them all unmasks none
     workspace:    as ``step``'s, for (B, L, V); default: one kept for the
                   current stream (while a CUDA graph is captured: one of the
                   graph's own, cleared in it)

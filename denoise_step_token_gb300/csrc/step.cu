@@ -536,7 +536,9 @@ __device__ __forceinline__ void warp_features(const float (&val)[NK], const bool
 // acquire instead, which does not hold back their stores.
 __shared__ int s_all_scanned;
 
-template <int NK>
+// kAbsent: masked positions may lack a token (tok < 0); those stay masked and
+// are candidates of no rule.
+template <int NK, bool kAbsent>
 __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool has_masked, int lane, bool direct) {
     // Row results arrive as zero-at-rest words (polled until they land);
     // requests without masked rows read only the launch's inputs.
@@ -549,6 +551,7 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
     float c[NK], cs_old[NK];
     unsigned long long rw[NK];
     bool msk[NK];
+    const auto cand = [&](int k) { return kAbsent ? msk[k] && tk[k] >= 0 : msk[k]; };
     bool any_masked = false, any_pass = false;
     float best_c = -INFINITY;
     int best_j = 0x7fffffff;
@@ -591,6 +594,7 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
             P.row_word[base + j] = 0ull;
             unpack_row(rw[k], c[k], tk[k]);
             any_masked = true;
+            if (kAbsent && tk[k] < 0) continue;
             if (c[k] > t) any_pass = true;
             // j grows with k, so a strict > keeps the lowest position on ties
             if (best_j == 0x7fffffff || c[k] > best_c) {
@@ -633,11 +637,11 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
             for (int src = 0; src < 32; ++src) {
                 const int jj = src + 32 * kk;
                 const float co = __shfl_sync(0xffffffffu, c[kk], src);
-                const bool mo = __shfl_sync(0xffffffffu, msk[kk] ? 1 : 0, src) != 0;
+                const bool mo = __shfl_sync(0xffffffffu, cand(kk) ? 1 : 0, src) != 0;
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {
                     const int j = lane + 32 * k;
-                    qrank[k] += (mo && msk[k] && (co > c[k] || (co == c[k] && jj < j))) ? 1 : 0;
+                    qrank[k] += (mo && cand(k) && (co > c[k] || (co == c[k] && jj < j))) ? 1 : 0;
                 }
             }
         }
@@ -652,7 +656,7 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
     for (int k = 0; k < NK; ++k) {
         const int j = lane + 32 * k;
         const bool valid = j < L;
-        const bool s = msk[k] && (P.quota ? qrank[k] < q : (c[k] > t || j == fb_j));
+        const bool s = cand(k) && (P.quota ? qrank[k] < q : (c[k] > t || j == fb_j));
         selk[k] = s;
         const int new_id = s ? tk[k] : id[k];
         float new_cs = 0.f;
@@ -739,13 +743,14 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
 }
 
 // direct: input_ids may be written at once (no other CTA still scans them).
+template <bool kAbsent = false>
 __device__ __forceinline__ void finalize_request(const StepParams& P, int b, bool has_masked, int lane,
                                                  bool direct = false) {
     const int nk = (P.L + 31) >> 5;
-    if (nk <= 1) finalize_request_t<1>(P, b, has_masked, lane, direct);
-    else if (nk <= 2) finalize_request_t<2>(P, b, has_masked, lane, direct);
-    else if (nk <= 4) finalize_request_t<4>(P, b, has_masked, lane, direct);
-    else finalize_request_t<32>(P, b, has_masked, lane, direct);
+    if (nk <= 1) finalize_request_t<1, kAbsent>(P, b, has_masked, lane, direct);
+    else if (nk <= 2) finalize_request_t<2, kAbsent>(P, b, has_masked, lane, direct);
+    else if (nk <= 4) finalize_request_t<4, kAbsent>(P, b, has_masked, lane, direct);
+    else finalize_request_t<32, kAbsent>(P, b, has_masked, lane, direct);
 }
 
 // ---------------------------------------------------------------------------
@@ -1493,7 +1498,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Step
     const int lane = threadIdx.x & 31;
     const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (b >= P.B) return;
-    bool any = false;
+    bool any = false, none = false;
     for (int j = lane; j < P.L; j += 32) {
         const long long r = (long long)b * P.L + j;
         if (P.ids[r] != P.mask_id) continue;
@@ -1506,6 +1511,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Step
             combine(M, S, mk, ts[k * stride + r]);
         }
         const float conf = __fdiv_rn(1.0f, S);
+        tok = max(tok, -1);
+        none = none || tok < 0;
         if (P.conf_out) P.conf_out[r] = conf;
         if (P.lse_out) P.lse_out[r] = M + logf(S);
         if (P.tok_out) P.tok_out[r] = tok;
@@ -1513,8 +1520,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Step
         st_relaxed_gpu_u64(P.row_word + r, pack_row(conf, tok));
     }
     any = __any_sync(0xffffffffu, any);
+    none = __any_sync(0xffffffffu, none);
     __syncwarp();
-    finalize_request(P, b, any, lane, true);
+    if (none) finalize_request<true>(P, b, any, lane, true);
+    else finalize_request(P, b, any, lane, true);
 }
 
 // per-device launch state, read without the lock on the launch path:

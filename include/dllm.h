@@ -222,8 +222,10 @@ int dllm_step_shard(const dllm_step_args* args, int32_t v0, float* m, float* s, 
  * finisher folds chunk partials (M = max, S = sum of s_k exp(m_k - M), the
  * first shard attaining M gives the token: the lowest global index), then
  * selection, update, done and features exactly as dllm_step (quota NULL:
- * threshold rule; else the fixed-steps rule).  args->logits is not read; the
- * workspace must be sized for (B, L, any V >= 1).  Errors as dllm_step, plus
+ * threshold rule; else the fixed-steps rule).  A position whose token comes
+ * out below 0 (idx -1: none) stays masked and is a candidate of neither rule;
+ * a request none of whose masked positions has a token unmasks nothing.
+ * args->logits is not read; the workspace must be sized for (B, L, any V >= 1).  Errors as dllm_step, plus
  * DLLM_ERR_INVAL for n_shards < 1, shard_stride < B * L or NULL triples. */
 int dllm_step_merge(const dllm_step_args* args, int32_t n_shards, const float* m, const float* s,
                     const int32_t* idx, int64_t shard_stride, const int32_t* quota, void* stream);

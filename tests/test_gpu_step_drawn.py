@@ -82,3 +82,66 @@ def test_a_caller_s_workspace(dllm):
     with pytest.raises(ValueError):
         dllm.step_sampled(tok, conf, ids, thr, cs, V=50, mask_id=50, workspace=ws.cpu())
     assert dllm.get_device_error(d) == 0
+
+
+def expected(ids, tok, conf, thr, quota, mask):
+    """(ids, n_new, done) by the rules of include/dllm.h, over the masked positions that have a token."""
+    ids = ids.copy()
+    n_new, done = [], []
+    for b in range(len(ids)):
+        at = np.flatnonzero((ids[b] == mask) & (tok[b] >= 0))
+        order = at[np.argsort(-conf[b, at], kind="stable")]
+        if quota is not None:
+            take = order[:max(int(quota[b]), 0)]
+        else:
+            over = at[conf[b, at] > thr[b]]
+            take = over if len(over) else order[:1]
+        ids[b, take] = tok[b, take]
+        n_new.append(len(take))
+        done.append(int(not (ids[b] == mask).any()))
+    return ids, n_new, done
+
+
+def run(dllm, ids, tok, conf, thr, quota, mask, V, **kw):
+    import torch
+    t = lambda x: None if x is None else torch.from_numpy(np.ascontiguousarray(x)).to(dev())  # noqa: E731
+    g_ids, cs = t(ids), torch.full(ids.shape, float("nan"), device=dev())
+    out = dllm.step_sampled(t(tok.ravel()), t(conf.ravel()), g_ids, t(thr), cs, V=V, mask_id=mask, quota=t(quota),
+                            debug=True, **kw)
+    assert dllm.get_device_error(dev()) == 0
+    return g_ids.cpu().numpy(), cs.cpu().numpy(), {k: v.cpu().numpy() for k, v in out.items()}
+
+
+@pytest.mark.parametrize("L", [1, 5, 32, 33, 100, 700])
+@pytest.mark.parametrize("rule", ["threshold", "negative threshold", "quota", "quota beyond"])
+def test_positions_without_a_token_stay_masked(dllm, rule, L):
+    """Some, then all, of a block's masked positions have no token: they are not unmasked by any rule, count for nothing,
+    and the block is not done."""
+    rng = np.random.default_rng(L)
+    B, V = 9, 50
+    mask = V
+    ids = np.where(rng.random((B, L)) < 0.7, mask, 3).astype(np.int32)
+    ids[0], ids[1], ids[2] = mask, mask, 3
+    tok = rng.integers(0, V, (B, L)).astype(np.int32)
+    conf = rng.random((B, L)).astype(np.float32)
+    none = rng.random((B, L)) < 0.4
+    none[0] = True                                       # a block without a token at all
+    none[1] = np.arange(L) > 0                           # a block with one
+    none[3] = False
+    tok[none] = np.where(rng.random(none.sum()) < 0.8, -1, -7)
+    conf[none] = np.where(rng.random(none.sum()) < 0.5, np.nan, 0.9)
+    conf[4] *= 0.1                                       # nothing passes: the surest one that has a token
+    thr = np.full(B, -1.0 if rule.startswith("negative") else 0.5, dtype=np.float32)
+    quota = None
+    if rule.startswith("quota"):
+        quota = np.full(B, L + 3 if "beyond" in rule else 2, dtype=np.int32)
+    want, n_new, done = expected(ids, tok, conf, thr, quota, mask)
+    got, cs, out = run(dllm, ids, tok, conf, None if quota is not None else thr, quota, mask, V)
+    np.testing.assert_array_equal(got, want)
+    assert (got >= 0).all() and got[0].tolist() == [mask] * L
+    assert out["n_new"].tolist() == n_new and out["done"].tolist() == done
+    assert out["accept_len"].tolist() == [L * d for d in done]
+    fresh = (ids == mask) & (want != mask)
+    np.testing.assert_allclose(cs[fresh], conf[fresh], rtol=2.0 ** -22)
+    assert np.isnan(cs[~fresh]).all()
+    np.testing.assert_array_equal(out["tok"], np.where(ids == mask, np.maximum(tok, -1), -1))
