@@ -201,6 +201,7 @@ _SIGNATURES = {
     "dllm_step_shard": (ctypes.c_int, [ctypes.POINTER(StepArgs), ctypes.c_int32, _p, _p, _p, _p]),
     "dllm_step_merge": (ctypes.c_int, [ctypes.POINTER(StepArgs), ctypes.c_int32, _p, _p, _p, ctypes.c_int64, _p,
                                        _p]),
+    "dllm_step_drawn": (ctypes.c_int, [ctypes.POINTER(StepArgs), _p, _p, _p, _p]),
     "dllm_step_vocab_shards": (ctypes.c_int, [ctypes.POINTER(StepArgs), ctypes.c_int32, ctypes.POINTER(VocabShard),
                                               _p, _p]),
     "dllm_predict_steps_stub": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _p, ctypes.c_int32, _p, _p, _p, _p]),
@@ -1093,7 +1094,7 @@ def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=
                  workspace=None):
     """The denoise step with drawn tokens (``sample``) in place of the argmax:
     selection by the probability of each draw, update, done and features as in
-    ``step`` (dllm_step_merge over one shard).
+    ``step`` (dllm_step_drawn) on the current stream.
 
     tokens, prob: int32 and float32 [B * L], read at the masked positions (the
                   others' rows may be skipped: -1 in ``sample``'s rows).  A
@@ -1102,8 +1103,8 @@ def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=
     workspace:    as ``step``'s, for (B, L, V); default: one kept for the
                   current stream (while a CUDA graph is captured: one of the
                   graph's own, cleared in it)
-    The other arguments and the outputs are those of ``step``; conf is the
-    draw's probability."""
+    The other arguments and the outputs are those of ``step``; conf is prob, bit
+    for bit."""
     torch = _torch()
     dev = _require_cuda(tokens, prob, input_ids, conf_state, thr, quota)
     B, L = input_ids.shape
@@ -1116,26 +1117,25 @@ def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=
     for name, t, dtype in (("thr", thr, torch.float32), ("quota", quota, torch.int32)):
         if t is not None and (t.dtype != dtype or t.numel() != B):
             raise TypeError(f"{name} must be {dtype} [{B}]")
-    m = torch.zeros(B * L, dtype=torch.float32, device=dev)
-    s = torch.where(prob > 0, 1.0 / prob, float("inf"))
+    if conf_state.numel() != B * L:
+        raise ValueError("conf_state needs one entry per position")
     out = {"done": torch.empty(B, dtype=torch.uint8, device=dev),
            "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
            "n_new": torch.empty(B, dtype=torch.int32, device=dev)}
     if feats:
         out["feats"] = torch.empty((B, NUM_FEATURES), dtype=torch.float32, device=dev)
     if debug:
-        out["conf"] = torch.full((B, L), float("nan"), dtype=torch.float32, device=dev)
-        out["tok"] = torch.full((B, L), -1, dtype=torch.int32, device=dev)
+        out["conf"] = torch.empty((B, L), dtype=torch.float32, device=dev)
+        out["tok"] = torch.empty((B, L), dtype=torch.int32, device=dev)
     lib = load()
     a = StepArgs(B=B, L=L, V=V, mask_id=mask_id, ldv=-(-V // 8) * 8, logits=None, input_ids=_ptr(input_ids), thr=_ptr(thr),
                  conf_state=_ptr(conf_state), done=_ptr(out["done"]), accept_len=_ptr(out["accept_len"]),
                  n_new=_ptr(out["n_new"]), feats=_ptr(out.get("feats")), conf_out=_ptr(out.get("conf")), lse_out=None,
                  tok_out=_ptr(out.get("tok")))
-    # the merge takes a workspace for any V: its own is for the least
-    need = int(lib.dllm_step_workspace_size(B, L, 1))
-    _check("dllm_step_merge", _call(torch, lambda args, stream: lib.dllm_step_merge(
-        args, 1, _ptr(m), _ptr(s), _ptr(tokens), B * L, _ptr(quota), stream), a, dev, _raw_stream(torch, dev), need,
-        workspace, _drawn_ws, need))
+    need = int(lib.dllm_step_workspace_size(B, L, 1))   # it takes a workspace for any V: its own is for the least
+    _check("dllm_step_drawn", _call(torch, lambda args, stream: lib.dllm_step_drawn(
+        args, _ptr(tokens), _ptr(prob), _ptr(quota), stream), a, dev, _raw_stream(torch, dev), need, workspace, _drawn_ws,
+        need))
     return out
 
 

@@ -1488,7 +1488,8 @@ __global__ void __launch_bounds__(256) features_kernel(int B, int L, int mask_id
 // Merge of vocabulary-shard triples, then S3-S6: one warp per request.
 // Shard k's triple of position r is at m/s/idx[k * stride + r]; the shards
 // are folded in order with the finisher's combine (so the lowest global
-// argmax wins ties when the shards ascend through the vocabulary).
+// argmax wins ties when the shards ascend through the vocabulary).  Without
+// ts, tm holds the positions' confidences and ti their tokens as they are.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ StepParams P, int n_shards,
                                                     const float* __restrict__ tm, const float* __restrict__ ts,
@@ -1503,18 +1504,25 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Step
         const long long r = (long long)b * P.L + j;
         if (P.ids[r] != P.mask_id) continue;
         any = true;
-        float M = -INFINITY, S = 0.f;
+        float conf, lse = __int_as_float(0x7fc00000);
         int tok = -1;
-        for (int k = 0; k < n_shards; ++k) {
-            const float mk = tm[k * stride + r];
-            if (mk > M || tok < 0) tok = ti[k * stride + r];
-            combine(M, S, mk, ts[k * stride + r]);
+        if (ts) {
+            float M = -INFINITY, S = 0.f;
+            for (int k = 0; k < n_shards; ++k) {
+                const float mk = tm[k * stride + r];
+                if (mk > M || tok < 0) tok = ti[k * stride + r];
+                combine(M, S, mk, ts[k * stride + r]);
+            }
+            conf = __fdiv_rn(1.0f, S);
+            lse = M + logf(S);
+        } else {
+            tok = ti[r];
+            conf = fmaxf(tm[r], 0.0f);   // NaN: 0
         }
-        const float conf = __fdiv_rn(1.0f, S);
         tok = max(tok, -1);
         none = none || tok < 0;
         if (P.conf_out) P.conf_out[r] = conf;
-        if (P.lse_out) P.lse_out[r] = M + logf(S);
+        if (P.lse_out) P.lse_out[r] = lse;
         if (P.tok_out) P.tok_out[r] = tok;
         P.row_tok[r] = tok;
         st_relaxed_gpu_u64(P.row_word + r, pack_row(conf, tok));
@@ -1800,12 +1808,15 @@ extern "C" int dllm_step_shard(const dllm_step_args* a, int32_t v0, float* m, fl
     return launch_step(a, nullptr, -1, &sh, stream);
 }
 
-extern "C" int dllm_step_merge(const dllm_step_args* a, int32_t n_shards, const float* m, const float* s,
-                               const int32_t* idx, int64_t shard_stride, const int32_t* quota, void* stream) {
+namespace dllm {
+namespace {
+// As dllm_step_merge; drawn: m holds confidences, there is no s.
+int launch_merge(const dllm_step_args* a, int32_t n_shards, const float* m, const float* s, const int32_t* idx,
+                 int64_t shard_stride, const int32_t* quota, bool drawn, void* stream) {
     if (!a || a->B < 0 || a->L < 1 || a->L > DLLM_MAX_L || a->V < 1) return DLLM_ERR_INVAL;
     if (a->B == 0) return DLLM_OK;
     if ((long long)a->B * a->L > 0x7fffffffLL || a->B >= (1 << 16)) return DLLM_ERR_UNSUPPORTED;
-    if (n_shards < 1 || !m || !s || !idx || shard_stride < (int64_t)a->B * a->L) return DLLM_ERR_INVAL;
+    if (n_shards < 1 || !m || (!s && !drawn) || !idx || shard_stride < (int64_t)a->B * a->L) return DLLM_ERR_INVAL;
     if (!a->input_ids || (!quota && !a->thr) || !a->conf_state || !a->done || !a->accept_len || !a->n_new)
         return DLLM_ERR_INVAL;
     if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0) return DLLM_ERR_WORKSPACE;
@@ -1830,6 +1841,18 @@ extern "C" int dllm_step_merge(const dllm_step_args* a, int32_t n_shards, const 
     DLLM_CUDA_TRY(launch_dependent(merge_kernel, dim3((a->B + wpb - 1) / wpb), dim3(wpb * 32), 0, as_stream(stream), P,
                                    n_shards, m, s, idx, (long long)shard_stride));
     return DLLM_OK;
+}
+}  // namespace
+}  // namespace dllm
+
+extern "C" int dllm_step_merge(const dllm_step_args* a, int32_t n_shards, const float* m, const float* s,
+                               const int32_t* idx, int64_t shard_stride, const int32_t* quota, void* stream) {
+    return launch_merge(a, n_shards, m, s, idx, shard_stride, quota, false, stream);
+}
+
+extern "C" int dllm_step_drawn(const dllm_step_args* a, const int32_t* tokens, const float* conf, const int32_t* quota,
+                               void* stream) {
+    return launch_merge(a, 1, conf, nullptr, tokens, a ? (int64_t)a->B * a->L : 0, quota, true, stream);
 }
 
 extern "C" int32_t dllm_transfer_quota(int32_t L, int32_t S, int32_t s) {

@@ -230,6 +230,15 @@ int dllm_step_shard(const dllm_step_args* args, int32_t v0, float* m, float* s, 
 int dllm_step_merge(const dllm_step_args* args, int32_t n_shards, const float* m, const float* s,
                     const int32_t* idx, int64_t shard_stride, const int32_t* quota, void* stream);
 
+/* S3-S6 over given tokens (dllm_sample's draws) in place of S2's argmax:
+ * tokens[r] and conf[r] (device int32 and float [B * L], read at the masked
+ * positions) are the token and confidence of position r, compared and recorded
+ * bit for bit (NaN and negative confidences count as 0).  tokens[r] < 0: none,
+ * as in dllm_step_merge.  lse_out receives NaN.  Everything else, the
+ * workspace and the errors are dllm_step_merge's. */
+int dllm_step_drawn(const dllm_step_args* args, const int32_t* tokens, const float* conf, const int32_t* quota,
+                    void* stream);
+
 /* The step over logits held as vocabulary shards, all on this device, in
  * one launch: what dllm_step_shard on every shard followed by
  * dllm_step_merge computes, bit for bit, without the triples' round trip or
@@ -921,8 +930,8 @@ int dllm_kv4_evict(const dllm_kv4_evict_args* args, void* stream);
 
 /* ======================================================================
  * Draws.  One token for each of N logits rows, by given random numbers: the
- * sampled counterpart of the step's argmax (S2); with dllm_step_merge (one
- * "shard", m = 0, s = 1 / prob, idx = tokens) the step commits drawn tokens.
+ * sampled counterpart of the step's argmax (S2); dllm_step_drawn commits drawn
+ * tokens by the step's rules.
  *
  * Entry i, over x = the V values of logits row r (r = rows[i], or i when rows
  * is NULL), T = temperature[i], in the order of falling values (ties: lowest

@@ -142,6 +142,27 @@ def test_positions_without_a_token_stay_masked(dllm, rule, L):
     assert out["n_new"].tolist() == n_new and out["done"].tolist() == done
     assert out["accept_len"].tolist() == [L * d for d in done]
     fresh = (ids == mask) & (want != mask)
-    np.testing.assert_allclose(cs[fresh], conf[fresh], rtol=2.0 ** -22)
+    np.testing.assert_array_equal(cs[fresh], conf[fresh])
     assert np.isnan(cs[~fresh]).all()
     np.testing.assert_array_equal(out["tok"], np.where(ids == mask, np.maximum(tok, -1), -1))
+
+
+def test_confidences_are_taken_as_they_are(dllm):
+    """Confidences next to their threshold, on either side and on it: compared and recorded bit for bit."""
+    rng = np.random.default_rng(1)
+    B, L, V = 200, 32, 50
+    mask = V
+    p = rng.random((B, L)).astype(np.float32)
+    thr = rng.random(B).astype(np.float32)
+    side = rng.integers(0, 3, (B, L))
+    p = np.where(side == 0, thr[:, None], np.where(side == 1, np.nextafter(thr[:, None], np.float32(2)), p))
+    p = np.where(p > thr[:, None], np.nextafter(thr[:, None], np.float32(2)), p).astype(np.float32)
+    p[5], p[6, ::2], p[7] = 1e-42, 0.0, np.float32(2.0 ** -149)      # subnormal ones count too
+    ids = np.full((B, L), mask, dtype=np.int32)
+    tok = rng.integers(0, V, (B, L)).astype(np.int32)
+    want, n_new, _ = expected(ids, tok, p, thr, None, mask)
+    got, cs, out = run(dllm, ids, tok, p, thr, None, mask, V)
+    np.testing.assert_array_equal(out["conf"], p)
+    np.testing.assert_array_equal(got, want)
+    assert out["n_new"].tolist() == n_new
+    np.testing.assert_array_equal(cs[want != mask], p[want != mask])

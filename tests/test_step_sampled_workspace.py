@@ -1,4 +1,4 @@
-"""The default workspace of step_sampled, on the CPU: which memory a call gets, and who else may be using it.
+"""step_sampled on the CPU: which memory a call gets as its workspace, who else may be using it, and what is refused.
 
 The library is replaced by one that records the workspace each call is given, and the checks that ask for a CUDA device
 are taken out."""
@@ -76,3 +76,21 @@ def test_a_caller_s_own(fake):
     for bad in (own.int(), own[::2]):
         with pytest.raises(ValueError):
             step(workspace=bad)
+
+
+@pytest.mark.parametrize("kw,code", [({"B": -1}, -1), ({"L": 0}, -1), ({"L": 1025}, -1), ({"V": 0}, -1), ({"input_ids": None}, -1),
+                                     ({"conf_state": None}, -1), ({"done": None}, -1), ({"thr": None}, -1),
+                                     ({"tokens": None}, -1), ({"conf": None}, -1), ({"workspace": None}, -5),
+                                     ({"workspace": 0x80010}, -5), ({"workspace_bytes": 64}, -5), ({"B": 1 << 16}, -6),
+                                     ({"B": 0, "tokens": None, "workspace": None}, 0)])
+def test_refusals(kw, code):
+    lib = pkg.load()
+    base = dict(B=2, L=4, V=50, mask_id=50, ldv=56, input_ids=0x10000, thr=0x20000, conf_state=0x30000, done=0x40000,
+                accept_len=0x50000, n_new=0x60000, workspace=0x80000, workspace_bytes=1 << 20, tokens=0x1000, conf=0x2000)
+    base.update(kw)
+    tokens, conf = base.pop("tokens"), base.pop("conf")
+    assert lib.dllm_step_drawn(ctypes.byref(pkg.StepArgs(**base)), tokens, conf, None, None) == code
+    if "thr" in kw:
+        base["workspace"] = None      # with a quota the threshold may be absent: refused for its workspace instead
+        assert lib.dllm_step_drawn(ctypes.byref(pkg.StepArgs(**base)), tokens, conf, 0x3000, None) == -5
+    assert lib.dllm_step_drawn(None, tokens, conf, None, None) == -1
