@@ -9,7 +9,8 @@
 // some hundred rows of a flat distribution.  A bf16 row holds few different
 // values, though: a histogram of its values is exact, each value's weight is
 // computed once, to 2^-44 in its exponent and 2^-62 in itself, and masses are
-// sums of count * weight in 64-bit fixed point.  The rest works on the histogram:
+// sums of count * weight in 64-bit fixed point, in units that leave room for V
+// tokens of the largest weight (2^-45 of it at 126464, 2^-33 at 2^28).  The rest works on the histogram:
 // what the filters leave, the mass, the value that the draw falls on, and which
 // of the tokens with that value, counted from the lowest, it is.
 //
@@ -293,7 +294,7 @@ __device__ __forceinline__ void count_at(uint32_t addr) {
     asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(addr));
 }
 
-__device__ __forceinline__ u64 warp_sum64(u64 v) {   // v < 2^59
+__device__ __forceinline__ u64 warp_sum64(u64 v) {   // the sum below 2^64
     const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7ffffffu);
     const uint32_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27) & 0x7ffffffu);
     const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 54));
@@ -535,17 +536,22 @@ __device__ __noinline__ void choose(float u, int k, float p) {
     using B = Bins<kWide>;
     Shared& sh = shared();
     u64 kept = B::seg_mass()[B::kCount - 1];
-    if (k > 0 && (uint32_t)k < B::seg_count()[B::kCount - 1]) {
+    const uint32_t count = B::seg_count()[B::kCount - 1];
+    bool last = false;   // what was found last is the last kept token
+    if (k > 0 && (uint32_t)k < count) {
         find<kWide>(true, (uint32_t)k);
         kept = sh.found.mass;
+        last = true;
         __syncwarp();
     }
     if (p < 1.0f) {
         find<kWide>(false, max(part_of(p, kept, true), 1ull));
         kept = min(kept, sh.found.mass);
+        last = true;
         __syncwarp();
     }
-    find<kWide>(false, u >= 0.0f ? (u < 1.0f ? min(part_of(u, kept, false) + 1, kept) : kept) : 1);
+    if (!(u >= 1.0f)) find<kWide>(false, u >= 0.0f ? min(part_of(u, kept, false) + 1, kept) : 1);
+    else if (!last) find<kWide>(true, count);   // by count: a last token's mass may round to nothing
     if (threadIdx.x == 0) sh.kept = kept;
 }
 

@@ -947,11 +947,16 @@ int dllm_kv4_evict(const dllm_kv4_evict_args* args, void* stream);
  * without a finite maximum (all -inf, or holding +inf or NaN) and a row number
  * outside [0, logits_rows) (-1: skip) give -1 and NaN.  NULL temperature is 1,
  * NULL top_k, top_p, min_p keep everything.
- * Cumulative masses are held to about 2^-40 of the whole (64-bit fixed point
- * over the counts of a row's different values), whatever V: the draw is the
- * definition's but where u lies that close to a border.  Tokens with weights
- * below 2^-62 of the largest are not drawn.  A row's result depends on that row
- * alone.  Serves sampling: no gradient. */
+ * Precision, in parts of the largest weight: a weight is good to 2^-40 of
+ * itself and to 2^-62; the mass of a row's tokens of one value is rounded to a
+ * unit of 2^(max(16, bits of V) - 62): 2^-46 to V = 65535, 2^-44 at 151936,
+ * 2^-33 at 2^28.  So a cumulative mass is off by 2^-40 of itself and half a unit
+ * for each different value in it at most (these cancel: 4000 values at 151936
+ * make about 2^-40), and the draw is the definition's but where u lies that
+ * close to a border.  Tokens with weights below 2^-62 are not kept; values
+ * whose tokens together weigh under half a unit are drawn only as the last kept
+ * one.  Temperatures above 0 count as 2^-126 at least.  A row's result depends
+ * on that row alone.  Serves sampling: no gradient. */
 typedef struct dllm_sample_args {
     int32_t N;                  /* entries (>= 0) */
     int32_t V;                  /* vocabulary size, 1..2^28 */
