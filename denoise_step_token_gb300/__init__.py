@@ -245,6 +245,7 @@ _SIGNATURES = {
     "dllm_kv4_attend": (ctypes.c_int, [ctypes.POINTER(Kv4AttendArgs), _p]),
     "dllm_kv4_evict": (ctypes.c_int, [ctypes.POINTER(Kv4EvictArgs), _p]),
     "dllm_sample": (ctypes.c_int, [ctypes.POINTER(SampleArgs), _p]),
+    "dllm_sample_conf": (ctypes.c_int, [ctypes.POINTER(SampleArgs), _p, _p]),
     "dllm_fp8_quantize": (ctypes.c_int, [ctypes.POINTER(Fp8QuantizeArgs), _p]),
     "dllm_fp8_matmul": (ctypes.c_int, [ctypes.POINTER(Fp8MatmulArgs), _p]),
     "dllm_pages_workspace_size": (_sz, [_i32, _i32]),
@@ -1048,9 +1049,9 @@ def kv4_evict(pages, weights, table, lens, keep, dst_table, *, recent=0):
 # ---------------------------------------------------------------------------
 # draws
 # ---------------------------------------------------------------------------
-def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=None, min_p=None):
+def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=None, min_p=None, conf=False):
     """Draw one token for each row of logits by given random numbers
-    (dllm_sample) on the current stream.
+    (dllm_sample; dllm_sample_conf with ``conf``) on the current stream.
 
     logits:      bf16 CUDA tensor of rows (last dimension the row stride,
                  16-byte rows), V (default: the stride) values each
@@ -1059,8 +1060,12 @@ def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=
                  row i
     temperature: float32 [N] (0: the most likely token), default 1
     top_k:       int32 [N] (0: all); top_p, min_p: float32 [N] (1 and 0: all)
-    Returns a dict: tokens (int32 [N], -1 for skipped and invalid rows) and
-    prob (float32 [N]), the probability with which each was drawn."""
+    conf:        also return each token's softmax probability (temperature 1,
+                 no filter): the confidence that ``step`` reports and
+                 ``step_sampled`` wants
+    Returns a dict: tokens (int32 [N], -1 for skipped and invalid rows), prob
+    (float32 [N]), the probability with which each was drawn (1 at temperature
+    0), and with ``conf`` conf (float32 [N])."""
     torch = _torch()
     dev = logits.device
     _check_tensors(torch, dev, logits, u, rows, temperature, top_k, top_p, min_p)
@@ -1081,7 +1086,11 @@ def sample(logits, u, *, V=None, rows=None, temperature=None, top_k=None, top_p=
                    u.data_ptr(), None if temperature is None else temperature.data_ptr(),
                    None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
                    None if min_p is None else min_p.data_ptr(), out["tokens"].data_ptr(), out["prob"].data_ptr())
-    rc = (_lib or load()).dllm_sample(ctypes.byref(a), _raw_stream(torch, dev))
+    if conf:
+        out["conf"] = torch.empty(N, dtype=float32, device=dev)
+        rc = (_lib or load()).dllm_sample_conf(ctypes.byref(a), out["conf"].data_ptr(), _raw_stream(torch, dev))
+    else:
+        rc = (_lib or load()).dllm_sample(ctypes.byref(a), _raw_stream(torch, dev))
     if rc:
         _check("dllm_sample", rc)
     return out
@@ -1093,12 +1102,15 @@ _drawn_ws = {}   # step_sampled's workspaces, a step's whole zero between calls
 def step_sampled(tokens, prob, input_ids, thr, conf_state, *, V, mask_id, feats=True, debug=False, quota=None,
                  workspace=None):
     """The denoise step with drawn tokens (``sample``) in place of the argmax:
-    selection by the probability of each draw, update, done and features as in
+    selection by each token's confidence, update, done and features as in
     ``step`` (dllm_step_drawn) on the current stream.
 
     tokens, prob: int32 and float32 [B * L], read at the masked positions (the
-                  others' rows may be skipped: -1 in ``sample``'s rows).  A
-                  masked position without a token (-1) stays masked and counts
+                  others' rows may be skipped: -1 in ``sample``'s rows).  prob
+                  is the confidence: ``sample``'s conf for that of ``step``, so
+                  that thresholds mean the same and greedy rows (temperature
+                  0) decode as in ``step``; ``sample``'s prob, the probability
+                  of the draw, is 1 wherever one token is kept.  A masked position without a token (-1) stays masked and counts
                   in neither rule: a block that lacks them all unmasks none
     workspace:    as ``step``'s, for (B, L, V); default: one kept for the
                   current stream (while a CUDA graph is captured: one of the

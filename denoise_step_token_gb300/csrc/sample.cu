@@ -1,5 +1,7 @@
 // dllm_sample: one token per logits row, drawn with temperature, top-k, min-p and
-// top-p by a given number u in [0, 1).
+// top-p by a given number u in [0, 1); dllm_sample_conf: also the token's softmax
+// probability, the step's confidence, from the same counts (its weights are a
+// second sum over the row's different values).
 //
 // Mathematics.  In the order of falling values (ties: lowest token first) with
 // w = exp((x - m) / T), every filter keeps a prefix, and the draw is the first
@@ -104,6 +106,7 @@ struct SampleParams {
     const float* min_p;
     int* tokens;
     float* prob;
+    float* conf;          // or NULL
     int* err;
     int cluster, slice;   // values of a CTA's slice
     int shift;            // masses are in units of 2^(shift - 62)
@@ -194,6 +197,7 @@ struct Shared {
     uint32_t warp_count[kWarps];
     uint32_t groups[64], counts[3];
     float part[kWarps];
+    u64 plain[kMaxCluster * kWarps];   // the first CTA's: sums of weights at temperature 1, a warp of the cluster each
     SliceFacts facts;
     Found found;
     u64 kept;
@@ -604,6 +608,60 @@ __device__ __noinline__ void sum_wide() {
     sync_warps();
 }
 
+// The row's mass at temperature 1 without filters, each warp's part into `plain` (the cluster's counting threads).
+__device__ __noinline__ void sum_plain(float top, int shift, int rank, int ctas) {
+    Shared& sh = shared();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Weights W;
+    W.shift = shift;
+    W.set(top, 1.0f, 0.0f);
+    u64 m = 0;
+#pragma unroll 1
+    for (int s = rank * kWarps + warp; s < kSegments; s += ctas * kWarps) {
+        const int o[1] = {s * 32 + lane};
+        uint32_t c[1];
+        counts_of(o, c, ctas);
+        if (__any_sync(0xffffffffu, c[0])) m += W.mass(c[0], W.of(Bins<false>::value(o[0]), sh.powers));
+    }
+    m = warp_sum64(m);
+    if (lane) return;
+    if (ctas > 1) peer_store64(smem_addr(&sh.plain[rank * kWarps + warp]), 0, m);
+    else sh.plain[warp] = m;
+}
+// The same on the wide path (every thread of the first CTA).
+__device__ __noinline__ void sum_plain_wide() {
+    using B = Bins<true>;
+    Shared& sh = shared();
+    Weights W = sh.row.W;
+    W.set(W.m, 1.0f, 0.0f);
+    u64 m = 0;
+#pragma unroll 1
+    for (int o0 = 0; o0 < 65536; o0 += kWindow) {
+        const float last = B::value(o0 + kWindow - 1), first = B::value(o0);
+        if (last > W.m) continue;
+        if (!isnan(first) && first < W.m && W.of(first, sh.powers) == 0) break;
+        count_keys(o0, kWindow);
+#pragma unroll 1
+        for (int o = threadIdx.x; o < kWindow; o += kThreads) {
+            const uint32_t n = word_at(kNegative + o * 4);
+            if (n) m += W.mass(n, W.of(B::value(o0 + o), sh.powers));
+        }
+        sync_warps();
+    }
+    m = warp_sum64(m);
+    if ((threadIdx.x & 31) == 0) sh.plain[threadIdx.x >> 5] = m;
+}
+// The found token's softmax probability, of the first `n` parts (one thread).
+__device__ __noinline__ float softmax_of(float top, int shift, int n) {
+    Shared& sh = shared();
+    Weights W;
+    W.set(top, 1.0f, 0.0f);
+    u64 all = 0;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) all += sh.plain[k];
+    return probability(W.of(__uint_as_float(sh.found.bits << 16), sh.powers), all, shift);
+}
+
 // Which of the first `have` halves of four words are 0, a bit each.
 __device__ __noinline__ uint32_t zero_halves(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int have) {
     uint32_t h = (a & 0xffffu) == 0 | (a >> 16 == 0) << 1 | ((b & 0xffffu) == 0) << 2 | (b >> 16 == 0) << 3;
@@ -766,6 +824,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
             if (rank == 0 && tid == 0) {
                 P.tokens[i] = -1;
                 P.prob[i] = __int_as_float(0x7fc00000);
+                if (P.conf) P.conf[i] = __int_as_float(0x7fc00000);
             }
             continue;
         }
@@ -915,6 +974,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
                     }
                 }
             }
+            if (P.conf) sum_plain(all.max, P.shift, rank, ctas);
         }
         if (ctas > 1) {
             meeting.arrive();
@@ -930,6 +990,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
                 sum_wide();
                 add_up<true>();
                 choose<true>(u, T == 0.0f ? 1 : k, p);
+                if (P.conf) sum_plain_wide();
             }
         }
         if (ctas > 1) {
@@ -964,6 +1025,8 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         if (rank == 0 && tid == kThreads - 32) {
             P.prob[i] = ok ? probability(sh.found.w, sh.kept, P.shift) : __int_as_float(0x7fc00000);
             if (!ok) P.tokens[i] = -1;
+            if (P.conf)
+                P.conf[i] = ok ? softmax_of(all.max, P.shift, wide ? kWarps : ctas * kWarps) : __int_as_float(0x7fc00000);
         }
         if (mine) locate(x, P.tokens + i, bits, r, count, l0, l1);
         if (ctas > 1) meeting.wait(&sh.abort, P.err);
@@ -981,7 +1044,8 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
 
 using namespace dllm;
 
-extern "C" int dllm_sample(const dllm_sample_args* a, void* stream) {
+namespace {
+int launch_sample(const dllm_sample_args* a, float* conf, void* stream) {
     if (!a || a->N < 0 || a->V < 1 || a->logits_rows < 0 || a->ldv < a->V) return DLLM_ERR_INVAL;
     if (a->N > 0 && ((a->logits_rows > 0 && !a->logits) || !a->u || !a->tokens || !a->prob)) return DLLM_ERR_INVAL;
     if ((reinterpret_cast<uintptr_t>(a->logits) & 15) || a->ldv % 8) return DLLM_ERR_ALIGN;
@@ -1003,6 +1067,7 @@ extern "C" int dllm_sample(const dllm_sample_args* a, void* stream) {
     P.min_p = a->min_p;
     P.tokens = a->tokens;
     P.prob = a->prob;
+    P.conf = conf;
     P.err = error_word_ptr();
     if (!P.err) return DLLM_ERR_CUDA;
     int c = 1;
@@ -1030,4 +1095,12 @@ extern "C" int dllm_sample(const dllm_sample_args* a, void* stream) {
     cfg.numAttrs = c > 1 ? 2 : 1;
     DLLM_CUDA_TRY(cudaLaunchKernelEx(&cfg, sample_kernel, P));
     return DLLM_OK;
+}
+}  // namespace
+
+extern "C" int dllm_sample(const dllm_sample_args* a, void* stream) { return launch_sample(a, nullptr, stream); }
+
+extern "C" int dllm_sample_conf(const dllm_sample_args* a, float* conf, void* stream) {
+    if (a && a->N > 0 && !conf) return DLLM_ERR_INVAL;
+    return launch_sample(a, conf, stream);
 }

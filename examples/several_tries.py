@@ -92,8 +92,8 @@ def decode(prompts, *, tries=3, L=8, blocks=3, V=2000, temperature=0.8, top_p=0.
             row = torch.where(ids.view(-1) == mask, row, torch.full_like(row, -1))
             logits = model.logits(att, row)
             drawn = dllm.sample(logits, torch.rand(n * L, generator=gen, device=dev), V=V, rows=row,
-                                temperature=full(temperature), top_p=full(top_p))
-            out = dllm.step_sampled(drawn["tokens"], drawn["prob"], ids, thr, conf, V=V, mask_id=mask)
+                                temperature=full(temperature), top_p=full(top_p), conf=True)
+            out = dllm.step_sampled(drawn["tokens"], drawn["conf"], ids, thr, conf, V=V, mask_id=mask)
             if bool(out["done"].all()):
                 break
         q, k, v = model.project(ids)                                     # the block as it was decided

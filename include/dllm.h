@@ -232,8 +232,8 @@ int dllm_step_merge(const dllm_step_args* args, int32_t n_shards, const float* m
 
 /* S3-S6 over given tokens (dllm_sample's draws) in place of S2's argmax:
  * tokens[r] and conf[r] (device int32 and float [B * L], read at the masked
- * positions) are the token and confidence of position r, compared and recorded
- * bit for bit (NaN and negative confidences count as 0).  tokens[r] < 0: none,
+ * positions) are the token and confidence of position r (dllm_sample_conf's for
+ * the step's own confidence), compared and recorded bit for bit (NaN and negative confidences count as 0).  tokens[r] < 0: none,
  * as in dllm_step_merge.  lse_out receives NaN.  Everything else, the
  * workspace and the errors are dllm_step_merge's. */
 int dllm_step_drawn(const dllm_step_args* args, const int32_t* tokens, const float* conf, const int32_t* quota,
@@ -975,6 +975,14 @@ typedef struct dllm_sample_args {
 
 /* Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA. */
 int dllm_sample(const dllm_sample_args* args, void* stream);
+
+/* dllm_sample, and conf[i] (device float [N]) = the softmax probability of
+ * tokens[i] over the whole row: temperature 1, no filter.  This is what
+ * dllm_step takes as a position's confidence, and what dllm_step_drawn wants
+ * where the step's thresholds are to mean the same: prob, the probability of the
+ * draw, is 1 for a greedy row or a single kept token however unsure the model
+ * is.  NaN where tokens[i] is -1. */
+int dllm_sample_conf(const dllm_sample_args* args, float* conf, void* stream);
 
 /* ======================================================================
  * Pages of a cache: who holds which.  For the 4-bit cache (dllm_kv4_*) and any

@@ -84,3 +84,35 @@ def test_large_vocabulary(dllm):
                 np.testing.assert_allclose(prob[i], p, rtol=1e-6)
             else:
                 assert abs(host[i][tokens[i]] - host[i][want]) < 0.1
+
+
+@pytest.mark.parametrize("kind", ["plain", "flat", "peaked", "masked", "zeros", "tiny", "huge", "edges", "lowest", "signed_zero"])
+@pytest.mark.parametrize("n,V", [(1, 126464), (3, 30011), (160, 5000), (700, 999), (2, 1)])
+def test_confidence(dllm, kind, n, V):
+    """conf against the softmax in 64 bits, whatever the draw's settings: a quotient of masses good to 1e-11 rounded once
+    to 32 bits (2^-24), weights held to 2^-62 of the largest.  Everything else is as without it."""
+    import torch
+    from test_gpu_sample import rows, settings
+    rng = np.random.default_rng(n)
+    x = rows(rng, n, V, kind)
+    if n > 2:
+        x[1] = -np.inf
+    u = rng.random(n)
+    logits = torch.full((n, -(-V // 8) * 8), float("nan"))
+    logits[:, :V] = torch.from_numpy(x.astype(np.float32))
+    logits = logits.to(torch.bfloat16).to(dev())
+    given = {k: torch.from_numpy(v).to(dev()) for k, v in settings(rng, n).items()}
+    given["temperature"][0] = -1.0 if n > 1 else 1.0
+    at = torch.from_numpy(np.where(rng.random(n) < 0.1, -1, np.arange(n)).astype(np.int32)).to(dev())
+    t = torch.from_numpy(u.astype(np.float32)).to(dev())
+    plain = dllm.sample(logits, t, V=V, rows=at, **given)
+    out = dllm.sample(logits, t, V=V, rows=at, conf=True, **given)
+    assert dllm.get_device_error(dev()) == 0
+    assert torch.equal(plain["tokens"], out["tokens"]) and torch.equal(plain["prob"].nan_to_num(-1), out["prob"].nan_to_num(-1))
+    tokens, conf = out["tokens"].cpu().numpy(), out["conf"].double().cpu().numpy()
+    for i in range(n):
+        if tokens[i] < 0:
+            assert np.isnan(conf[i])
+            continue
+        w = np.exp(x[i].astype(np.float64) - x[i].max())
+        np.testing.assert_allclose(conf[i], w[tokens[i]] / w.sum(), rtol=1e-7, atol=2.0 ** -62)

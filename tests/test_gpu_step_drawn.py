@@ -166,3 +166,49 @@ def test_confidences_are_taken_as_they_are(dllm):
     np.testing.assert_array_equal(got, want)
     assert out["n_new"].tolist() == n_new
     np.testing.assert_array_equal(cs[want != mask], p[want != mask])
+
+
+@pytest.mark.parametrize("quota", [False, True])
+@pytest.mark.parametrize("L,V", [(8, 500), (32, 30011), (5, 126464)])
+def test_greedy_rows_decode_as_the_step_does(dllm, quota, L, V):
+    """At temperature 0 (and top-k 1) the draw and its conf are the step's argmax and confidence: the same positions are
+    unmasked, in a batch where other requests are sampled.  Requests where a confidence lies within 1e-5 of what decides (the
+    step's own tolerance) are left out; few do."""
+    import torch
+    rng = np.random.default_rng(L)
+    B, mask = 24, V
+    ldv = -(-V // 8) * 8
+    x = rng.standard_normal((B * L, ldv)) * 2
+    x[np.arange(B * L), rng.integers(0, V, B * L)] += rng.random(B * L) * (8 + np.log(V))
+    logits = torch.from_numpy(x).to(torch.bfloat16).to(dev())
+    ids0 = np.where(rng.random((B, L)) < 0.7, mask, 3).astype(np.int32)
+    ids0[0] = 3
+    thr = torch.full((B,), 0.6, device=dev())
+    left = torch.full((B,), 2, dtype=torch.int32, device=dev()) if quota else None
+    ids, cs = torch.from_numpy(ids0).to(dev()), torch.full((B, L), float("nan"), device=dev())
+    mine, mine_cs = ids.clone(), cs.clone()
+    want = dllm.step(logits, ids, thr, cs, V=V, mask_id=mask, quota=left, debug=True)
+    masked = torch.from_numpy(ids0.ravel() == mask).to(dev())
+    rows = torch.where(masked, torch.arange(B * L, dtype=torch.int32, device=dev()), -1).to(torch.int32)
+    T = torch.zeros(B * L, device=dev())
+    k = torch.zeros(B * L, dtype=torch.int32, device=dev())
+    T[B * L // 2:], k[B * L // 2:] = 0.9, 1                  # the other greedy requests, by top-k
+    T[:L * 3], k[:L * 3] = 1.0, 0                            # three sampled ones
+    d = dllm.sample(logits, torch.rand(B * L, device=dev()), V=V, rows=rows, temperature=T, top_k=k, conf=True)
+    out = dllm.step_sampled(d["tokens"], d["conf"], mine, thr, mine_cs, V=V, mask_id=mask, quota=left, debug=True)
+    assert dllm.get_device_error(dev()) == 0
+    p, conf = want["conf"].cpu().numpy(), out["conf"].cpu().numpy()
+    compared = 0
+    for b in range(3, B):
+        at = ids0[b] == mask
+        np.testing.assert_array_equal(want["tok"][b].cpu().numpy()[at], out["tok"][b].cpu().numpy()[at])
+        np.testing.assert_allclose(conf[b, at], p[b, at], rtol=0, atol=1e-5)
+        order = np.sort(p[b, at])
+        if not at.any() or np.abs(p[b, at] - 0.6).min() < 1e-5 or (len(order) > 1 and np.diff(order).min() < 1e-5):
+            continue
+        compared += 1
+        assert torch.equal(mine[b], ids[b]) and int(out["n_new"][b]) == int(want["n_new"][b])
+        assert int(out["done"][b]) == int(want["done"][b])
+        fresh = (ids0[b] == mask) & (ids[b].cpu().numpy() != mask)
+        np.testing.assert_allclose(mine_cs[b].cpu().numpy()[fresh], cs[b].cpu().numpy()[fresh], rtol=0, atol=1e-5)
+    assert compared >= B // 2

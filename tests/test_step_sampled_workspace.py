@@ -94,3 +94,14 @@ def test_refusals(kw, code):
         base["workspace"] = None      # with a quota the threshold may be absent: refused for its workspace instead
         assert lib.dllm_step_drawn(ctypes.byref(pkg.StepArgs(**base)), tokens, conf, 0x3000, None) == -5
     assert lib.dllm_step_drawn(None, tokens, conf, None, None) == -1
+
+
+def test_sample_conf_refusals():
+    lib = pkg.load()
+    a = pkg.SampleArgs(N=2, V=16, ldv=16, logits_rows=2, logits=0x10000, u=0x20000, tokens=0x30000, prob=0x40000)
+    assert lib.dllm_sample_conf(ctypes.byref(a), None, None) == -1
+    assert lib.dllm_sample_conf(None, 0x50000, None) == -1
+    a.ldv = 20
+    assert lib.dllm_sample_conf(ctypes.byref(a), 0x50000, None) == -2
+    a.N, a.ldv = 0, 16
+    assert lib.dllm_sample_conf(ctypes.byref(a), None, None) == 0
