@@ -536,9 +536,7 @@ __device__ __forceinline__ void warp_features(const float (&val)[NK], const bool
 // acquire instead, which does not hold back their stores.
 __shared__ int s_all_scanned;
 
-// kAbsent: masked positions may lack a token (tok < 0); those stay masked and
-// are candidates of no rule.
-template <int NK, bool kAbsent>
+template <int NK>
 __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool has_masked, int lane, bool direct) {
     // Row results arrive as zero-at-rest words (polled until they land);
     // requests without masked rows read only the launch's inputs.
@@ -551,7 +549,6 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
     float c[NK], cs_old[NK];
     unsigned long long rw[NK];
     bool msk[NK];
-    const auto cand = [&](int k) { return kAbsent ? msk[k] && tk[k] >= 0 : msk[k]; };
     bool any_masked = false, any_pass = false;
     float best_c = -INFINITY;
     int best_j = 0x7fffffff;
@@ -594,7 +591,6 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
             P.row_word[base + j] = 0ull;
             unpack_row(rw[k], c[k], tk[k]);
             any_masked = true;
-            if (kAbsent && tk[k] < 0) continue;
             if (c[k] > t) any_pass = true;
             // j grows with k, so a strict > keeps the lowest position on ties
             if (best_j == 0x7fffffff || c[k] > best_c) {
@@ -637,11 +633,11 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
             for (int src = 0; src < 32; ++src) {
                 const int jj = src + 32 * kk;
                 const float co = __shfl_sync(0xffffffffu, c[kk], src);
-                const bool mo = __shfl_sync(0xffffffffu, cand(kk) ? 1 : 0, src) != 0;
+                const bool mo = __shfl_sync(0xffffffffu, msk[kk] ? 1 : 0, src) != 0;
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {
                     const int j = lane + 32 * k;
-                    qrank[k] += (mo && cand(k) && (co > c[k] || (co == c[k] && jj < j))) ? 1 : 0;
+                    qrank[k] += (mo && msk[k] && (co > c[k] || (co == c[k] && jj < j))) ? 1 : 0;
                 }
             }
         }
@@ -656,7 +652,7 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
     for (int k = 0; k < NK; ++k) {
         const int j = lane + 32 * k;
         const bool valid = j < L;
-        const bool s = cand(k) && (P.quota ? qrank[k] < q : (c[k] > t || j == fb_j));
+        const bool s = msk[k] && (P.quota ? qrank[k] < q : (c[k] > t || j == fb_j));
         selk[k] = s;
         const int new_id = s ? tk[k] : id[k];
         float new_cs = 0.f;
@@ -743,14 +739,13 @@ __device__ __noinline__ void finalize_request_t(const StepParams& P, int b, bool
 }
 
 // direct: input_ids may be written at once (no other CTA still scans them).
-template <bool kAbsent = false>
 __device__ __forceinline__ void finalize_request(const StepParams& P, int b, bool has_masked, int lane,
                                                  bool direct = false) {
     const int nk = (P.L + 31) >> 5;
-    if (nk <= 1) finalize_request_t<1, kAbsent>(P, b, has_masked, lane, direct);
-    else if (nk <= 2) finalize_request_t<2, kAbsent>(P, b, has_masked, lane, direct);
-    else if (nk <= 4) finalize_request_t<4, kAbsent>(P, b, has_masked, lane, direct);
-    else finalize_request_t<32, kAbsent>(P, b, has_masked, lane, direct);
+    if (nk <= 1) finalize_request_t<1>(P, b, has_masked, lane, direct);
+    else if (nk <= 2) finalize_request_t<2>(P, b, has_masked, lane, direct);
+    else if (nk <= 4) finalize_request_t<4>(P, b, has_masked, lane, direct);
+    else finalize_request_t<32>(P, b, has_masked, lane, direct);
 }
 
 // ---------------------------------------------------------------------------
@@ -1472,16 +1467,101 @@ __device__ __forceinline__ void features_one(int b, int L, int mask_id, const in
     warp_features<NK>(val, inU, L, lane, feats + (long long)b * DLLM_NUM_FEATURES);
 }
 
-__global__ void __launch_bounds__(256) features_kernel(int B, int L, int mask_id, const int* ids, const float* cs,
-                                                      float* feats) {
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (b >= B) return;
+__device__ __noinline__ void features_of(int b, int L, int mask_id, const int* ids, const float* cs, float* feats, int lane) {
     const int nk = (L + 31) >> 5;
     if (nk <= 1) features_one<1>(b, L, mask_id, ids, cs, feats, lane);
     else if (nk <= 2) features_one<2>(b, L, mask_id, ids, cs, feats, lane);
     else if (nk <= 4) features_one<4>(b, L, mask_id, ids, cs, feats, lane);
     else features_one<32>(b, L, mask_id, ids, cs, feats, lane);
+}
+
+__global__ void __launch_bounds__(256) features_kernel(int B, int L, int mask_id, const int* ids, const float* cs,
+                                                      float* feats) {
+    const int lane = threadIdx.x & 31;
+    const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (b < B) features_of(b, L, mask_id, ids, cs, feats, lane);
+}
+
+// S3-S6 for a request (one warp) with masked positions that have no token
+// (tok < 0): they stay masked and are candidates of no rule.  Apart from the
+// registers' form above and by plain loops over the workspace: few requests come
+// here, and another instance of it doubles this file's compile time.
+__device__ __noinline__ void finalize_absent(const StepParams& P, int b, int lane) {
+    const int L = P.L;
+    int* const ids = P.ids + (long long)b * L;
+    float* const cs = P.cs + (long long)b * L;
+    unsigned long long* const words = P.row_word + (long long)b * L;
+    unsigned char* const sel = P.sel + (long long)b * L;
+    const float t = P.quota ? 0.f : P.thr[b];
+    const int q = P.quota ? P.quota[b] : 0;
+    // whether position j is a candidate, and its confidence and token
+    auto candidate = [&](int j, float& c, int& tok) {
+        if (ids[j] != P.mask_id) return false;
+        unpack_row(ld_relaxed_gpu_u64(words + j), c, tok);
+        return tok >= 0;
+    };
+    float c, bc = -INFINITY;
+    int tok, bj = 0x7fffffff;
+    bool pass = false;
+    for (int j = lane; j < L; j += 32) {
+        if (!candidate(j, c, tok)) continue;
+        pass = pass || c > t;
+        if (bj == 0x7fffffff || c > bc) {
+            bc = c;
+            bj = j;
+        }
+    }
+    pass = __any_sync(0xffffffffu, pass);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        const float oc = __shfl_xor_sync(0xffffffffu, bc, off);
+        const int oj = __shfl_xor_sync(0xffffffffu, bj, off);
+        if (oj != 0x7fffffff && (bj == 0x7fffffff || oc > bc || (oc == bc && oj < bj))) {
+            bc = oc;
+            bj = oj;
+        }
+    }
+    for (int j = lane; j < L; j += 32) {
+        bool s = candidate(j, c, tok);
+        if (s && P.quota) {
+            int ahead = 0;
+            float oc;
+            int ot;
+            for (int i = 0; i < L && ahead < q; ++i)
+                if (candidate(i, oc, ot) && (oc > c || (oc == c && i < j))) ++ahead;
+            s = ahead < q;
+        } else if (s) {
+            s = c > t || (!pass && j == bj);
+        }
+        sel[j] = s ? 1 : 0;
+    }
+    __syncwarp();   // ids and words change from here on
+    int n_sel = 0;
+    bool still = false;
+    for (int j = lane; j < L; j += 32) {
+        if (ids[j] == P.mask_id) {
+            if (sel[j]) {
+                unpack_row(ld_relaxed_gpu_u64(words + j), c, tok);
+                ids[j] = tok;
+                cs[j] = c;
+                ++n_sel;
+            }
+            words[j] = 0ull;
+        } else {
+            if (P.conf_out) P.conf_out[(long long)b * L + j] = __int_as_float(0x7fc00000);
+            if (P.lse_out) P.lse_out[(long long)b * L + j] = __int_as_float(0x7fc00000);
+            if (P.tok_out) P.tok_out[(long long)b * L + j] = -1;
+        }
+        still = still || ids[j] == P.mask_id;
+    }
+    n_sel = __reduce_add_sync(0xffffffffu, n_sel);
+    const bool done = !__any_sync(0xffffffffu, still);
+    if (lane == 0) {
+        P.done[b] = done ? 1 : 0;
+        P.accept[b] = done ? L : 0;
+        P.n_new[b] = n_sel;
+    }
+    if (P.feats) features_of(b, L, P.mask_id, P.ids, P.cs, P.feats, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1530,7 +1610,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Step
     any = __any_sync(0xffffffffu, any);
     none = __any_sync(0xffffffffu, none);
     __syncwarp();
-    if (none) finalize_request<true>(P, b, any, lane, true);
+    if (none) finalize_absent(P, b, lane);
     else finalize_request(P, b, any, lane, true);
 }
 

@@ -145,6 +145,16 @@ def test_positions_without_a_token_stay_masked(dllm, rule, L):
     np.testing.assert_array_equal(cs[fresh], conf[fresh])
     assert np.isnan(cs[~fresh]).all()
     np.testing.assert_array_equal(out["tok"], np.where(ids == mask, np.maximum(tok, -1), -1))
+    import torch
+    cs0 = np.where(ids == mask, np.float32("nan"), rng.random((B, L)).astype(np.float32))
+    t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(dev())  # noqa: E731
+    g_ids, g_cs = t(ids), t(cs0)
+    again = dllm.step_sampled(t(tok.ravel()), t(conf.ravel()), g_ids, None if quota is not None else t(thr), g_cs, V=V,
+                              mask_id=mask, quota=None if quota is None else t(quota))
+    np.testing.assert_array_equal(g_ids.cpu().numpy(), want)
+    feats = dllm.features(g_ids, g_cs, mask_id=mask)
+    np.testing.assert_array_equal(again["feats"].cpu().numpy(), feats.cpu().numpy())
+    assert np.isfinite(again["feats"][1:].cpu().numpy()[(want[1:] != mask).any(1)]).all()
 
 
 def test_confidences_are_taken_as_they_are(dllm):
