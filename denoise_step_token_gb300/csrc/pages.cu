@@ -179,25 +179,58 @@ __device__ __forceinline__ int fork_tokens(const ForkParams& P, int s) {
 }
 
 // Forks that end inside a page take a free one, in their order; from the first that finds none on they are not served.
+// Nor is one whose rows or pages are outside: its tables' entries are looked through first, a warp's lanes over each of its
+// forks in turn (neighbouring forks in different warps), so that it takes no page.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ ForkParams P) {
     pdl_wait();
     pdl_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int f0 = 0; f0 < P.F; f0 += kThreads) {
+        const int f = f0 + lane * (kThreads / 32) + warp;
+        int s = 0, pages = 0;   // the fork's source and the pages that it takes over
+        bool ok = false;
+        if (f < P.F) {
+            s = __ldg(P.src + f);
+            ok = P.T.row_ok(s) && P.T.row_ok(__ldg(P.dst + f));
+            if (ok) {
+                const int n = fork_tokens(P, s);
+                pages = n / P.T.page_size + (n % P.T.page_size != 0);
+            }
+        }
+        uint32_t bad = 0;   // a bit for each of the warp's forks
+        const uint32_t some = __ballot_sync(0xffffffffu, pages > 0);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 4) {   // four forks' loads at once
+            if ((some >> i0 & 15) == 0) continue;
+            const int* row[4];
+            int most[4], page[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                most[k] = __shfl_sync(0xffffffffu, pages, i0 + k);
+                row[k] = P.T.table + (long long)__shfl_sync(0xffffffffu, s, i0 + k) * P.T.max_pages;
+                page[k] = lane < most[k] ? row[k][lane] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bool out = (unsigned)page[k] >= (unsigned)P.T.n_pages;
+#pragma unroll 4
+                for (int j = lane + 32; j < most[k]; j += 32) out |= (unsigned)row[k][j] >= (unsigned)P.T.n_pages;
+                if (out) bad |= 1u << (i0 + k);
+            }
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        if (f < P.F) P.fresh[f] = P.T.ok(!(bad >> lane & 1)) && ok ? 0 : -2;
+    }
+    __syncthreads();
     int need = 0;
     for (int f0 = 0; f0 < P.F; f0 += kThreads) {
         const int f = f0 + threadIdx.x;
         int from = -1;
         bool ok = false;
-        if (f < P.F) {
-            const int s = __ldg(P.src + f), d = __ldg(P.dst + f);
-            ok = P.T.row_ok(s) && P.T.row_ok(d);
-            if (ok) {
-                const int n = fork_tokens(P, s), full = n / P.T.page_size;
-                if (n % P.T.page_size) {
-                    from = P.T.table[(long long)s * P.T.max_pages + full];
-                    ok = P.T.page_ok(from);
-                    if (!ok) from = -1;
-                }
-            }
+        if (f < P.F && P.fresh[f] == 0) {
+            ok = true;
+            const int s = __ldg(P.src + f), n = fork_tokens(P, s);
+            if (n % P.T.page_size) from = P.T.table[(long long)s * P.T.max_pages + n / P.T.page_size];
         }
         int total;
         const int rank = need + block_before(from >= 0, &total);
