@@ -1467,7 +1467,11 @@ __device__ __forceinline__ void features_one(int b, int L, int mask_id, const in
     warp_features<NK>(val, inU, L, lane, feats + (long long)b * DLLM_NUM_FEATURES);
 }
 
-__device__ __noinline__ void features_of(int b, int L, int mask_id, const int* ids, const float* cs, float* feats, int lane) {
+__global__ void __launch_bounds__(256) features_kernel(int B, int L, int mask_id, const int* ids, const float* cs,
+                                                      float* feats) {
+    const int lane = threadIdx.x & 31;
+    const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (b >= B) return;
     const int nk = (L + 31) >> 5;
     if (nk <= 1) features_one<1>(b, L, mask_id, ids, cs, feats, lane);
     else if (nk <= 2) features_one<2>(b, L, mask_id, ids, cs, feats, lane);
@@ -1475,11 +1479,62 @@ __device__ __noinline__ void features_of(int b, int L, int mask_id, const int* i
     else features_one<32>(b, L, mask_id, ids, cs, feats, lane);
 }
 
-__global__ void __launch_bounds__(256) features_kernel(int B, int L, int mask_id, const int* ids, const float* cs,
-                                                      float* feats) {
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (b < B) features_of(b, L, mask_id, ids, cs, feats, lane);
+// The features of request b by plain loops, bit for bit those of warp_features.
+__device__ __forceinline__ void features_plain(const StepParams& P, int b, int lane) {
+    const int L = P.L;
+    const int* const ids = P.ids + (long long)b * L;
+    const float* const cs = P.cs + (long long)b * L;
+    int n = 0;
+    float sum = 0.f;
+    for (int j = lane; j < L; j += 32) {
+        if (ids[j] == P.mask_id) continue;
+        ++n;
+        sum += cs[j];
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, off);
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    }
+    float* const out = P.feats + (long long)b * DLLM_NUM_FEATURES;
+    if (n == 0) {
+        if (lane < 6) out[lane] = lane < 5 ? __int_as_float(0x7fc00000) : 0.f;
+        return;
+    }
+    // ranks 0 and lo, hi of the three quantiles: 0.25 t (n - 1)
+    int want[7] = {};
+    float frac[3], got[7] = {};
+    uint32_t have = 0;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        const float h = 0.25f * float(t + 1) * float(n - 1);
+        want[1 + 2 * t] = int(floorf(h));
+        want[2 + 2 * t] = min(want[1 + 2 * t] + 1, n - 1);
+        frac[t] = h - floorf(h);
+    }
+    for (int j = lane; j < L; j += 32) {
+        if (ids[j] == P.mask_id) continue;
+        const float v = cs[j];
+        int rank = 0;
+        for (int i = 0; i < L; ++i)
+            if (ids[i] != P.mask_id && (cs[i] < v || (cs[i] == v && i < j))) ++rank;
+#pragma unroll
+        for (int t = 0; t < 7; ++t)
+            if (rank == want[t]) {
+                got[t] = v;
+                have |= 1u << t;
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < 7; ++t)
+        got[t] = __shfl_sync(0xffffffffu, got[t], __ffs(__ballot_sync(0xffffffffu, have >> t & 1)) - 1);
+    if (lane != 0) return;
+    out[0] = got[0];
+    out[1] = got[1] + frac[0] * (got[2] - got[1]);
+    out[2] = got[3] + frac[1] * (got[4] - got[3]);
+    out[3] = sum / float(n);
+    out[4] = got[5] + frac[2] * (got[6] - got[5]);
+    out[5] = float(n) / float(L);
 }
 
 // S3-S6 for a request (one warp) with masked positions that have no token
@@ -1561,7 +1616,8 @@ __device__ __noinline__ void finalize_absent(const StepParams& P, int b, int lan
         P.accept[b] = done ? L : 0;
         P.n_new[b] = n_sel;
     }
-    if (P.feats) features_of(b, L, P.mask_id, P.ids, P.cs, P.feats, lane);
+    __syncwarp();
+    if (P.feats) features_plain(P, b, lane);
 }
 
 // ---------------------------------------------------------------------------
