@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const __grid_constant__ 
             P.taken[r] = more;
             P.start[r] = rank;
         }
-        need = min(need + total, P.T.n_pages + 1);
+        need = (int)min((long long)need + total, P.T.n_pages + 1ll);   // 2^30 and 2^30 may meet
     }
     const int have = list_free(P.T.refs, P.T.n_pages, min(need, P.T.n_pages), P.list);
     if (have < need && threadIdx.x == 0) set_error(P.T.err, DLLM_DEVERR_PAGE);

@@ -46,3 +46,21 @@ def test_forks_of_long_rows_are_checked_to_their_end(dllm):
     assert s.g_held[2:].tolist() == [4000, 0] * 550
     assert torch.equal(s.g_table[2::2, :4000], s.g_table[:1, :4000].expand(550, -1))
     assert torch.equal(s.g_refs[s.g_table[0, :4000].long()], torch.full((4000,), 551, dtype=torch.int32, device=s.dev))
+
+
+def test_growth_at_the_limits_of_its_sums(dllm):
+    """The largest pool, full, and rounds of rows that want 2^30 pages each: nobody is served, and that is recorded."""
+    import torch
+    dev = torch.device("cuda", 0)
+    n_pages, R, most = 2 ** 30 - 1, 2048, 2 ** 20
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 24 GB")
+    refs = torch.ones(n_pages, dtype=torch.int32, device=dev)
+    table = torch.empty(R, most, dtype=torch.int32, device=dev)
+    held, lens = torch.zeros(R, dtype=torch.int32, device=dev), torch.full((R,), most, dtype=torch.int32, device=dev)
+    rows = torch.arange(R, dtype=torch.int32, device=dev)
+    taken = dllm.page_grow(refs, table, held, lens, rows, 0, page_size=1)
+    assert bool((taken == -1).all()) and not held.any()
+    assert dllm.get_device_error(dev) == 5
+    del refs, table
+    torch.cuda.empty_cache()
