@@ -57,8 +57,9 @@ __device__ __forceinline__ uint32_t top_bits(const uint4& q) {
     for (int k = 0; k < 4; ++k) t = max(t, max(w[k] & 0xffffu, w[k] >> 16));
     return t;
 }
+constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126
 __device__ __forceinline__ float scale_of(uint32_t top) {
-    return top >= 0x7f80u ? __int_as_float(0x7fc00000) : fmaxf(__fdiv_rn(__uint_as_float(top << 16), 448.0f), 1.17549435e-38f);
+    return top >= 0x7f80u ? __int_as_float(0x7fc00000) : fmaxf(__fdiv_rn(__uint_as_float(top << 16), 448.0f), kLeastScale);
 }
 // x / scale to the nearest code, for 8 values.  The quotient is the correctly rounded one, as the definition has it.
 __device__ __forceinline__ uint2 codes_of(const uint4& q, float scale) {
@@ -267,7 +268,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_matmul_kernel(const __grid_co
             float sa_next = __ldg(sa), sb_next = __ldg(sb);
             for (int b = 0; b < P.blocks; ++b, ++n) {
                 const uint32_t buf = n & 1;
-                const unsigned long long s2 = f32x2_splat(sa_next * sb_next);
+                // The scales' product, where it is a normal number.  Where it is not, the sum is multiplied by one after the
+                // other: above 2^128 by the smaller (>= 1) first, below 2^-126 by the larger (< 2^23) first, so that nothing
+                // passes the range on the way unless the result does.  Scales of 2^-126 (kLeastScale) are left with the
+                // product: they belong to groups of zeros, and the multiplications cost 1030 us for 880 where a warp
+                // has such a row (1851 x 151936 x 3584).
+                const float both = sa_next * sb_next, lo = fminf(sa_next, sb_next), hi = fmaxf(sa_next, sb_next);
+                const bool small = fabsf(both) < kLeastScale;
+                const bool alone = (small && lo != kLeastScale) || fabsf(both) == INFINITY;
+                const bool apart = __any_sync(0xffffffffu, alone);
+                const unsigned long long s2 = f32x2_splat(alone ? small ? lo : hi : both);
+                const unsigned long long first = f32x2_splat(alone ? small ? hi : lo : 1.0f);
                 if (b + 1 < P.blocks) {
                     sa_next = __ldg(sa + b + 1);
                     sb_next = __ldg(sb + b + 1);
@@ -289,6 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_matmul_kernel(const __grid_co
                         if (lane == 0)
                             asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_leader(smem_addr(&sh.read[buf])))
                                          : "memory");
+                    }
+                    if (apart) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const unsigned long long y =
+                                f32x2_mul(f32x2_pack(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), first);
+                            v[2 * c] = __float_as_uint(f32x2_lo(y));
+                            v[2 * c + 1] = __float_as_uint(f32x2_hi(y));
+                        }
                     }
 #pragma unroll
                     for (int c = 0; c < 8; ++c)

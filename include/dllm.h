@@ -1093,7 +1093,11 @@ int dllm_fp8_quantize(const dllm_fp8_quantize_args* args, void* stream);
  * a[m][k] b[n][k], g the groups of 128 columns, rounded to bf16 once.  The
  * inner sums and the outer one are held in 32 bits, groups in ascending order:
  * an output depends on its two rows alone, and equal calls give equal bits.
- * Columns N up to the next multiple of 8 receive 0.
+ * Columns N up to the next multiple of 8 receive 0.  The two scales' product may
+ * pass the range of 32 bits, a group's scaled sum and the sum over groups may not
+ * (they become infinite).  Where one scale is 2^-126 itself (the quantiser's for
+ * groups of zeros and of values up to 448 2^-126) and the other below 1, the
+ * product is rounded to a subnormal number: that group's part is good to 2^-125.
  *   - K, lda and ldb multiples of 16, ldo of 8 and at least N rounded up to 8;
  *     a, b and out 16-byte aligned.
  * Serves inference: no gradient.  Errors: DLLM_ERR_INVAL, DLLM_ERR_ALIGN,
