@@ -106,7 +106,7 @@ struct SampleParams {
     const float* min_p;
     int* tokens;
     float* prob;
-    float* conf;          // or NULL
+    float* conf;          // (kConf)
     int* err;
     int cluster, slice;   // values of a CTA's slice
     int shift;            // masses are in units of 2^(shift - 62)
@@ -757,6 +757,8 @@ __device__ __forceinline__ void count_word(uint32_t w, uint32_t base, uint32_t& 
     count_at(base + (at >> 16));
 }
 
+// kConf: with the softmax probability (in the same kernel, unused, it cost the plain draw 2 %: code to fetch).
+template <bool kConf>
 __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __grid_constant__ SampleParams P) {
     Shared& sh = shared();
     const uint32_t base = smem_addr(smem);
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
             if (rank == 0 && tid == 0) {
                 P.tokens[i] = -1;
                 P.prob[i] = __int_as_float(0x7fc00000);
-                if (P.conf) P.conf[i] = __int_as_float(0x7fc00000);
+                if constexpr (kConf) P.conf[i] = __int_as_float(0x7fc00000);
             }
             continue;
         }
@@ -974,7 +976,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
                     }
                 }
             }
-            if (P.conf) sum_plain(all.max, P.shift, rank, ctas);
+            if constexpr (kConf) sum_plain(all.max, P.shift, rank, ctas);
         }
         if (ctas > 1) {
             meeting.arrive();
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
                 sum_wide();
                 add_up<true>();
                 choose<true>(u, T == 0.0f ? 1 : k, p);
-                if (P.conf) sum_plain_wide();
+                if constexpr (kConf) sum_plain_wide();
             }
         }
         if (ctas > 1) {
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         if (rank == 0 && tid == kThreads - 32) {
             P.prob[i] = ok ? probability(sh.found.w, sh.kept, P.shift) : __int_as_float(0x7fc00000);
             if (!ok) P.tokens[i] = -1;
-            if (P.conf)
+            if constexpr (kConf)
                 P.conf[i] = ok ? softmax_of(all.max, P.shift, wide ? kWarps : ctas * kWarps) : __int_as_float(0x7fc00000);
         }
         if (mine) locate(x, P.tokens + i, bits, r, count, l0, l1);
@@ -1077,8 +1079,9 @@ int launch_sample(const dllm_sample_args* a, float* conf, void* stream) {
     int bits = 0;   // V tokens of mass 2^(62 - shift) stay below 2^62
     while ((1ll << bits) <= a->V) ++bits;
     P.shift = std::max(16, bits);
-    static SmemOnce done;
-    DLLM_CUDA_TRY(allow_smem(sample_kernel, kSmem, done));
+    const auto kernel = conf ? sample_kernel<true> : sample_kernel<false>;
+    static SmemOnce done[2];
+    DLLM_CUDA_TRY(allow_smem(kernel, kSmem, done[conf ? 1 : 0]));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(a->N, sms * kPerSm / c) * c);
     cfg.blockDim = dim3(kThreads + 32);
@@ -1093,7 +1096,7 @@ int launch_sample(const dllm_sample_args* a, float* conf, void* stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c > 1 ? 2 : 1;
-    DLLM_CUDA_TRY(cudaLaunchKernelEx(&cfg, sample_kernel, P));
+    DLLM_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, P));
     return DLLM_OK;
 }
 }  // namespace
