@@ -94,3 +94,32 @@ def test_quantised_rows_of_any_size(dllm):
         qb, sb = dllm.fp8_quantize(y.to(d), block_rows=128)
         got = check(dllm, qa.float().cpu(), sa.cpu(), qb.float().cpu(), sb.cpu())
         assert not got[7].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 20, 144), (300, 513, 512)])
+def test_rows_that_lie_apart(dllm, M, N, K):
+    """Strides of both operands above K and of the output above N: the same bits as of packed ones, what lies between left
+    as it was and never read (codes of NaN)."""
+    import ctypes
+    import torch
+    d = torch.device("cuda", 0)
+    gen = torch.Generator().manual_seed(M)
+    e4m3 = torch.float8_e4m3fn
+    blocks = -(-K // 128)
+    a, b = codes(gen, M, K).to(e4m3), codes(gen, N, K).to(e4m3)
+    sa, sb = torch.rand(M, blocks, generator=gen).to(d), torch.rand(-(-N // 128), blocks, generator=gen).to(d)
+    want = dllm.fp8_matmul(a.to(d), sa, b.to(d), sb)
+
+    def apart(x, pad):
+        wide = torch.full((x.shape[0] + 1, K + pad), 0x7F, dtype=torch.uint8)
+        wide[:-1, :K] = x.view(torch.uint8)
+        return wide.to(d)
+    wa, wb = apart(a, 48), apart(b, 16)
+    ldo = -(-N // 8) * 8 + 24
+    out = torch.full((M, ldo), 7.0, dtype=torch.bfloat16, device=d)
+    args = dllm.Fp8MatmulArgs(M, N, K, 0, K + 48, K + 16, ldo, wa.data_ptr(), sa.data_ptr(), wb.data_ptr(), sb.data_ptr(),
+                              out.data_ptr())
+    assert dllm.load().dllm_fp8_matmul(ctypes.byref(args), torch.cuda.current_stream().cuda_stream) == 0
+    assert dllm.get_device_error(d) == 0
+    edge = want.shape[1]
+    assert torch.equal(out[:, :edge], want) and bool((out[:, edge:] == 7).all())

@@ -64,3 +64,31 @@ def test_growth_at_the_limits_of_its_sums(dllm):
     assert dllm.get_device_error(dev) == 5
     del refs, table
     torch.cuda.empty_cache()
+
+
+def test_copies_within_one_pool(dllm):
+    """Source and destination in the same tensors: disjoint pages, several copies of one, skipped ones."""
+    rng = np.random.default_rng(4)
+    s = State(rng, 100, 2, 8, 16, [100, 17], arrays=((4096 + 48,), (16,), (3, 32)))
+    order = rng.permutation(100)
+    src, dst = order[:40].copy(), order[40:80].copy()
+    src[7:12] = src[3]
+    src[20], dst[21] = -1, -1
+    dllm.page_copy(s.g_pools, s.g_pools, s.rows(src), s.rows(dst))
+    for a in s.pools:
+        for x, y in zip(src, dst):
+            if x >= 0 and y >= 0:
+                a[y] = a[x]
+    s.same(dllm)
+
+
+@pytest.mark.parametrize("n_pages", [40, 9000])
+def test_pools_without_arrays(dllm, n_pages):
+    """Tables and counts alone, where the contents are someone else's: forks, release, compaction."""
+    rng = np.random.default_rng(5)
+    s = State(rng, n_pages, 4, 10, 16, [40, 16, 33, 20], arrays=(), spare_rows=3)
+    s.fork(dllm, [0, 2, 0], [4, 5, 6])
+    s.free(dllm, [0, 1])
+    s.compact(dllm)
+    s.grow(dllm, [2, 4], 50)
+    s.compact(dllm)
