@@ -1206,7 +1206,11 @@ def page_fork(pools, refs, table, held, lens, src, dst, *, page_size):
     table: int32 [B, max_pages]; held, lens: int32 [B] pages and tokens of each
            request (all updated for the rows ``dst``, which must hold none)
     src, dst: int32 [F]; no dst twice, none among the src
-    Returns int32 [F]: the page each fork took, -1 none, -2 not served."""
+    Forks share the attention weights of the pages that they share: requests
+    holding a page in common must not be given ``weights`` in one
+    ``kv4_attend``.
+    Returns int32 [F]: the page each fork took, -1 none, -2 not served (a row or
+    page out of range, or no page left)."""
     torch = _torch()
     dev = refs.device
     batch = _pages_batch(torch, refs, table, held, page_size)
@@ -1344,7 +1348,8 @@ def fp8_matmul(a, a_scale, b, b_scale, *, out=None):
     a, a_scale: float8_e4m3fn [M, K] and float32 [M, ceil(K / 128)]
     b, b_scale: float8_e4m3fn [N, K] and float32 [ceil(N / 128), ceil(K / 128)]
     out:        bf16 [M, at least N rounded up to 8], or None: a new one of that
-                width (columns from N on are 0)
+                width (columns from N to the next multiple of 8 are 0, later
+                ones left as they are)
     Returns out: rows that the step, sample and token_logprobs take as logits."""
     torch = _torch()
     dev = a.device

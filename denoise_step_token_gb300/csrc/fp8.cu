@@ -14,14 +14,16 @@
 // pair saves is L2 traffic: 32 KB a CTA and block; single CTAs with 128 x 256 tiles
 // would need 48.
 // What bounds it: those sums, about 1000 cycles a block with the barriers on both
-// sides (tensor pipes 53 % active).  1851 x 151936 x 3584: 887 us, 2270 TFLOP/s; 21 x
-// 126464 x 4096: 143 us, 3.6 TB/s of weights.  With 8 warps of sums and 128 columns a
-// thread 1037 and 187 us.
+// sides (tensor pipes 53 % active).  1851 x 151936 x 3584: 857 us over the same operands again and
+// again, 900 in a graph with others, 960 over changing ones (2350 to 2100 TFLOP/s: the card's power); 21 x
+// 126464 x 4096: 120 to 150 us, 4.3 to 3.5 TB/s of weights.  With 8 warps of sums and 128 columns a
+// thread 1037 and 187 us, where this form then took 996 and 143.
 // Two TMEM buffers of 256 columns: a block's sums are read while the next block's
 // are formed.  Six stages of 32 KB in shared memory.
 // Tiles run along the rows of A first: the CTAs in flight share few tiles of B, which
-// comes from DRAM once, and A stays in L2.  For few rows the tile is the same: its
-// products cost less than reading the weights.
+// comes from DRAM once, and A stays in L2.  For few rows the tile is the same, though its
+// sums, of rows that are not there for the most part, then take longer than reading the
+// weights (77 us); no other tile has been measured.
 #include <cuda.h>
 #include <math.h>
 #include <stdint.h>

@@ -27,7 +27,8 @@
 // 151936 values: 270 us (2.1 TB/s; on the way there, at 292: without the search 238, without the
 // counters' atomics too 123).
 // CTAs a row: as many as fill the SMs, none with under 4096 values.  More than
-// needed cost: 353 us for clusters of two in that batch.
+// needed cost: 353 us for clusters of two in that batch, the only one where the
+// rule's other side was measured.
 #include <math.h>
 #include <stdint.h>
 
@@ -933,7 +934,8 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm) sample_kernel(const __g
         Weights W;
         W.shift = P.shift;
         W.set(all.max, T == 0.0f ? 1.0f : T, T == 0.0f ? 0.0f : min_p);
-        // low values count where their weights do: -256 is the largest
+        // low values count where their weights may: -256 is the largest (-inf is counted with them, so from a temperature of
+        // (256 + maximum) / 55 on a row with masked tokens goes the wide path too)
         const bool wide = all.other || (all.low > 0 && W.rough(-256.0f) > -80.0f);
         if (tid == 0) sh.row = RowFacts{W, x, P.V, ctas};
         if (ok && !wide) {

@@ -1032,7 +1032,12 @@ int dllm_pages_copy(const dllm_pages_pool* from, const dllm_pages_pool* to, int3
  * -2 for a fork that is not served (a row or page out of range, or no page left
  * for it: then none of the later ones that need a page is served either): its
  * lens and held become 0.  No dst twice, and none among the src; a src may
- * occur any number of times. */
+ * occur any number of times.
+ * Attention weights among the pool's arrays are the page's, so forks share those
+ * of the pages that they share: dllm_kv4_attend must not be given weights for
+ * requests that hold a page in common in one call (see there), and what one
+ * writes the others find.  Thin a cache (dllm_kv4_evict) before it is forked, or
+ * copy a fork's shared pages to pages of its own first (dllm_pages_copy). */
 int dllm_pages_fork(const dllm_pages_batch* batch, const dllm_pages_pool* pool, int32_t* lens, int32_t F,
                     const int32_t* src, const int32_t* dst, int32_t* fresh, void* workspace, size_t workspace_bytes,
                     void* stream);
