@@ -14,8 +14,8 @@
 // pair saves is L2 traffic: 32 KB a CTA and block; single CTAs with 128 x 256 tiles
 // would need 48.
 // What bounds it: those sums, about 1000 cycles a block with the barriers on both
-// sides (tensor pipes 53 % active).  1851 x 151936 x 3584: 857 us over the same operands again and
-// again, 900 in a graph with others, 960 over changing ones (2350 to 2100 TFLOP/s: the card's power); 21 x
+// sides (tensor pipes 53 % active).  1851 x 151936 x 3584: 870 us over the same operands again and
+// again, 900 in a graph with others, 960 over changing ones (2320 to 2100 TFLOP/s: the card's power); 21 x
 // 126464 x 4096: 120 to 150 us, 4.3 to 3.5 TB/s of weights.  With 8 warps of sums and 128 columns a
 // thread 1037 and 187 us, where this form then took 996 and 143.
 // Two TMEM buffers of 256 columns: a block's sums are read while the next block's
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_matmul_kernel(const __grid_co
                 // has such a row (1851 x 151936 x 3584).
                 const float both = sa_next * sb_next, lo = fminf(sa_next, sb_next), hi = fmaxf(sa_next, sb_next);
                 const bool small = fabsf(both) < kLeastScale;
-                const bool alone = (small && lo != kLeastScale) || fabsf(both) == INFINITY;
+                const bool alone = (small && lo > 0.0f && lo != kLeastScale) || fabsf(both) == INFINITY;   // (0: the product is 0)
                 const bool apart = __any_sync(0xffffffffu, alone);
                 const unsigned long long s2 = f32x2_splat(alone ? small ? lo : hi : both);
                 const unsigned long long first = f32x2_splat(alone ? small ? hi : lo : 1.0f);

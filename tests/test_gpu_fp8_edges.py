@@ -66,6 +66,21 @@ def test_small_scales(dllm, ea, eb):
     check(dllm, a, sa, b, sb)
 
 
+def test_scales_of_zero(dllm):
+    """A scale of 0 makes its part 0, whatever finite scale it meets."""
+    import torch
+    gen = torch.Generator().manual_seed(12)
+    M, N, K = 140, 300, 256
+    a, b = codes(gen, M, K), codes(gen, N, K)
+    sa, sb = torch.rand(M, 2, generator=gen) + 0.5, torch.full((3, 2), 2.0 ** 110)
+    sa[::3], sb[1] = 0, 0
+    sa[1] = 2.0 ** -100
+    got = check(dllm, a, sa * 2.0 ** -10, b, sb)
+    assert not got[::3].any() and not got[:, 128:256].any() and got[1, :128].any()
+    sa[:], sb[:] = 2.0 ** 120, 0
+    assert not check(dllm, a, sa, b, sb).any()
+
+
 def test_least_scale(dllm):
     """Rows at the quantiser's least scale, beside ordinary ones: zeros stay zeros, others are good to what is promised."""
     import torch
